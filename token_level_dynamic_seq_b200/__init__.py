@@ -40,6 +40,10 @@ EXPORTED = ("logo_num_selected", "logo_workspace_size", "logo_workspace_init", "
             "logo_backward", "logo_forward_host_buffer_size", "logo_forward_host", "logo_build_flags")
 
 
+# The 8-bit cache's entry points (include/logo_cache8.h).
+EXPORTED_CACHE8 = ("logo_cache8_append", "logo_cache8_read", "logo_decode8_workspace_size", "logo_decode8")
+
+
 class LogoError(RuntimeError):
     def __init__(self, status: int, message: str):
         self.status = status
@@ -50,6 +54,14 @@ class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("L", ctypes.c_int),
                 ("d", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p), ("nseq", ctypes.c_int),
                 ("max_seqlen", ctypes.c_int)]
+
+
+class Cache8Desc(ctypes.Structure):
+    """logo_cache8 of include/logo_cache8.h."""
+    _fields_ = [("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("Lmax", ctypes.c_int), ("d", ctypes.c_int),
+                ("block", ctypes.c_int), ("type", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("k_tail", ctypes.c_void_p),
+                ("v_tail", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -70,6 +82,7 @@ def load_library(path: str | None = None):
         vp, i32, i64, dbl, flt, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_double,
                                       ctypes.c_float, ctypes.c_size_t)
         sp = ctypes.POINTER(Shape)
+        cp = ctypes.POINTER(Cache8Desc)
         sig = {
             "logo_num_selected": ([dbl, i64], i64),
             "logo_workspace_size": ([sp, dbl], sz),
@@ -95,6 +108,10 @@ def load_library(path: str | None = None):
             "logo_forward_host": ([vp, vp, vp, vp, sp, i32, dbl, flt, vp, vp, vp, vp, sz, vp], i32),
             "logo_backward": ([vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, sp, i32, flt, vp, vp, vp,
                                vp, vp, sz, vp], i32),
+            "logo_cache8_append": ([cp, vp, vp, sp, vp, vp, vp, sz, vp], i32),
+            "logo_cache8_read": ([cp, vp, sp, vp, vp, vp, sz, vp], i32),
+            "logo_decode8_workspace_size": ([cp, i32, i32], sz),
+            "logo_decode8": ([vp, cp, vp, vp, vp, i32, i32, i32, flt, vp, vp, vp, sz, vp], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -426,3 +443,7 @@ def useful_flops(d: int, Hq: int, seqlens, window: int, sel_positions) -> tuple[
         lp += w * (w + 1) // 2 + (n - w) * w
     sp = int(sum(int(p) + 1 for p in sel_positions))
     return 4 * d * Hq * lp, 4 * d * Hq * sp
+
+
+from .kvcache import (Cache8, cache8, cache8_append, cache8_read, decode8,  # noqa: E402
+                      decode8_workspace)

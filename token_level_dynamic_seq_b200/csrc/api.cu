@@ -12,8 +12,10 @@
 #include <cstring>
 #include <mutex>
 
+#include "cache8.cuh"
 #include "kernels.cuh"
 #include "logo.h"
+#include "logo_cache8.h"
 
 namespace {
 
@@ -365,6 +367,93 @@ cudaError_t copy_rows(void* dst, size_t dst_pitch, const void* src, size_t src_p
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+// ---------------------------------------------------------------- 8-bit cache
+
+logo_status check_ptr(const void* p, const char* name, unsigned align)
+{
+    if (!p) return fail(LOGO_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) & (align - 1))
+        return fail(LOGO_ERR_INVALID_ARG, "%s is not %u-byte aligned", name, align);
+    return LOGO_OK;
+}
+
+// `buffers`: whether the codes and scales are looked at too.
+logo_status check_cache(const logo_cache8* c, bool buffers = true)
+{
+    if (!c) return fail(LOGO_ERR_INVALID_ARG, "cache is NULL");
+    if (c->d != 64 && c->d != 128) return fail(LOGO_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", c->d);
+    if (c->block != 64 && c->block != 128)
+        return fail(LOGO_ERR_UNSUPPORTED, "scale block of %d tokens (supported: 64, 128)", c->block);
+    if (c->type != LOGO_CACHE_E4M3 && c->type != LOGO_CACHE_INT8)
+        return fail(LOGO_ERR_UNSUPPORTED, "cache type %d (supported: e4m3, int8)", c->type);
+    if (c->B < 1 || c->Hkv < 1 || c->Lmax < 1)
+        return fail(LOGO_ERR_INVALID_ARG, "B=%d Hkv=%d Lmax=%d out of range", c->B, c->Hkv, c->Lmax);
+    if (c->Lmax > (1 << 30) || (long long)c->B * c->Hkv > (1 << 20))
+        return fail(LOGO_ERR_UNSUPPORTED, "Lmax=%d above 2^30 or B*Hkv=%lld above 2^20", c->Lmax,
+                    (long long)c->B * c->Hkv);
+    logo_status st;
+    if (!buffers) return LOGO_OK;
+    if ((st = check_ptr(c->k, "cache k", 16)) != LOGO_OK || (st = check_ptr(c->v, "cache v", 16)) != LOGO_OK ||
+        (st = check_ptr(c->k_scale, "k_scale", 4)) != LOGO_OK ||
+        (st = check_ptr(c->v_scale, "v_scale", 4)) != LOGO_OK)
+        return st;
+    return LOGO_OK;
+}
+
+// The rows of an append or a read: one sequence of `shape` per sequence of the cache.
+logo_status check_rows_of(const logo_cache8* c, const logo_shape* sh, Geo& g)
+{
+    logo_status st = check_shape(sh, g);
+    if (st != LOGO_OK) return st;
+    if (g.Hkv != c->Hkv || g.d != c->d || g.nseq != c->B)
+        return fail(LOGO_ERR_INVALID_ARG, "rows of %d sequences, Hkv=%d, d=%d for a cache of %d, Hkv=%d, d=%d", g.nseq,
+                    g.Hkv, g.d, c->B, c->Hkv, c->d);
+    return LOGO_OK;
+}
+
+logo_status check_rows8(const logo_cache8* c, int Hq, int n)
+{
+    if (Hq < 1 || n < 1) return fail(LOGO_ERR_INVALID_ARG, "Hq=%d n=%d out of range", Hq, n);
+    if (Hq % c->Hkv != 0) return fail(LOGO_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, c->Hkv);
+    if ((long long)(Hq / c->Hkv) * n > logo::kDec8MaxRows)
+        return fail(LOGO_ERR_UNSUPPORTED, "Hq/Hkv * n = %lld query rows (at most %d)", (long long)(Hq / c->Hkv) * n,
+                    logo::kDec8MaxRows);
+    return LOGO_OK;
+}
+
+logo::Cache8View view_of(const logo_cache8* c)
+{
+    logo::Cache8View v;
+    v.code[0] = static_cast<uint8_t*>(c->k);
+    v.code[1] = static_cast<uint8_t*>(c->v);
+    v.scale[0] = c->k_scale;
+    v.scale[1] = c->v_scale;
+    v.tail[0] = c->k_tail;
+    v.tail[1] = c->v_tail;
+    v.B = c->B;
+    v.Hkv = c->Hkv;
+    v.Lmax = c->Lmax;
+    v.nblk = (c->Lmax + c->block - 1) / c->block;
+    return v;
+}
+
+// Codes as bytes [slabs][rows][d], box d x kDec8Stage x 1, swizzled over the whole row.
+logo_status make_map8(CUtensorMap* map, const void* base, int d, int rows, int slabs)
+{
+    logo_status st;
+    EncodeTiledFn fn = encode_fn(st);
+    if (!fn) return st;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)slabs};
+    cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)d * (cuuint64_t)rows};
+    cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)logo::kDec8Stage, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(LOGO_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return LOGO_OK;
 }
 
 }  // namespace
@@ -747,6 +836,118 @@ logo_status logo_decode(const logo_bf16* q, const logo_bf16* k_cache, const logo
     }
     NvtxRange range("logo decode");
     cudaError_t e = logo::launch_decode(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LOGO_OK : cuda_fail(e, "decode launch");
+}
+
+size_t logo_decode8_workspace_size(const logo_cache8* cache, int Hq, int n)
+{
+    if (check_cache(cache, false) != LOGO_OK || check_rows8(cache, Hq, n) != LOGO_OK) return 0;
+    return kWsHeaderBytes + logo::decode8_partials_bytes(cache->B, cache->Hkv, Hq / cache->Hkv * n, cache->d);
+}
+
+logo_status logo_cache8_append(const logo_cache8* cache, const logo_bf16* k, const logo_bf16* v,
+                               const logo_shape* shape, const int32_t* start, int32_t* new_len, void* ws,
+                               size_t ws_bytes, logo_stream_t stream)
+{
+    Geo g;
+    logo_status st;
+    if ((st = check_cache(cache)) != LOGO_OK || (st = check_rows_of(cache, shape, g)) != LOGO_OK) return st;
+    if ((st = check_ws(ws, ws_bytes)) != LOGO_OK) return st;
+    if ((st = check_ptr(cache->k_tail, "k_tail", 32)) != LOGO_OK ||
+        (st = check_ptr(cache->v_tail, "v_tail", 32)) != LOGO_OK ||
+        (st = check_ptr(start, "start", 4)) != LOGO_OK)
+        return st;
+    if (g.L > 0 && ((st = check_ptr(k, "k", 32)) != LOGO_OK || (st = check_ptr(v, "v", 32)) != LOGO_OK)) return st;
+    if (new_len && (st = check_ptr(new_len, "new_len", 4)) != LOGO_OK) return st;
+    if (new_len == start) return fail(LOGO_ERR_INVALID_ARG, "new_len must not be start");
+    logo::Append8Params p;
+    memset(&p, 0, sizeof p);
+    p.c = view_of(cache);
+    p.src[0] = k;
+    p.src[1] = v;
+    p.start = start;
+    p.cu_seqlens = g.cu;
+    p.new_len = new_len;
+    p.status = static_cast<uint32_t*>(ws);
+    p.n = g.L;
+    p.max_n = g.max_len;
+    p.nb = (int)(((long long)g.max_len + 2 * cache->block - 2) / cache->block);  // a block's last row first
+    NvtxRange range("logo cache append");
+    cudaError_t e = logo::launch_append8(p, cache->type, cache->d, cache->block, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LOGO_OK : cuda_fail(e, "cache append launch");
+}
+
+logo_status logo_cache8_read(const logo_cache8* cache, const int32_t* start, const logo_shape* shape,
+                             logo_bf16* k_out, logo_bf16* v_out, void* ws, size_t ws_bytes, logo_stream_t stream)
+{
+    Geo g;
+    logo_status st;
+    if ((st = check_cache(cache)) != LOGO_OK || (st = check_rows_of(cache, shape, g)) != LOGO_OK) return st;
+    if ((st = check_ws(ws, ws_bytes)) != LOGO_OK) return st;
+    if ((st = check_ptr(start, "start", 4)) != LOGO_OK) return st;
+    if (g.L > 0 && ((st = check_ptr(k_out, "k_out", 32)) != LOGO_OK || (st = check_ptr(v_out, "v_out", 32)) != LOGO_OK))
+        return st;
+    logo::Read8Params p;
+    memset(&p, 0, sizeof p);
+    p.c = view_of(cache);
+    p.dst[0] = k_out;
+    p.dst[1] = v_out;
+    p.start = start;
+    p.cu_seqlens = g.cu;
+    p.status = static_cast<uint32_t*>(ws);
+    p.n = g.L;
+    p.max_n = g.max_len;
+    NvtxRange range("logo cache read");
+    cudaError_t e = logo::launch_read8(p, cache->type, cache->d, cache->block, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LOGO_OK : cuda_fail(e, "cache read launch");
+}
+
+logo_status logo_decode8(const logo_bf16* q, const logo_cache8* cache, const int32_t* cache_len, const float* gate,
+                         const float* tau, int Hq, int n, int window, float scale, logo_bf16* out, int32_t* selected,
+                         void* ws, size_t ws_bytes, logo_stream_t stream)
+{
+    logo_status st;
+    float sl2;
+    if ((st = check_cache(cache)) != LOGO_OK || (st = check_rows8(cache, Hq, n)) != LOGO_OK) return st;
+    if (window < 1) return fail(LOGO_ERR_INVALID_ARG, "window=%d must be >= 1", window);
+    if ((st = resolve_scale(scale, cache->d, sl2)) != LOGO_OK) return st;
+    if ((st = check_ws(ws, ws_bytes)) != LOGO_OK) return st;
+    const int R = Hq / cache->Hkv * n;
+    const size_t need = kWsHeaderBytes + logo::decode8_partials_bytes(cache->B, cache->Hkv, R, cache->d);
+    if (ws_bytes < need) return fail(LOGO_ERR_WORKSPACE, "workspace of %zu bytes, decode needs %zu", ws_bytes, need);
+    if ((st = check_ptr(q, "q")) != LOGO_OK || (st = check_ptr(out, "out")) != LOGO_OK ||
+        (st = check_ptr(cache_len, "cache_len", 4)) != LOGO_OK || (st = check_ptr(gate, "gate", 4)) != LOGO_OK ||
+        (st = check_ptr(tau, "tau", 4)) != LOGO_OK)
+        return st;
+    if (selected && (st = check_ptr(selected, "selected", 4)) != LOGO_OK) return st;
+    logo::Decode8Params p;
+    memset(&p, 0, sizeof p);
+    const int slabs = cache->B * cache->Hkv;
+    if ((st = make_map8(&p.tm_k, cache->k, cache->d, cache->Lmax, slabs)) != LOGO_OK ||
+        (st = make_map8(&p.tm_v, cache->v, cache->d, cache->Lmax, slabs)) != LOGO_OK)
+        return st;
+    p.q = q;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.cache_len = cache_len;
+    p.gate = gate;
+    p.tau = tau;
+    p.out = out;
+    p.selected = selected;
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes);
+    p.status = static_cast<uint32_t*>(ws);
+    p.B = cache->B;
+    p.Hkv = cache->Hkv;
+    p.R = R;
+    p.n = n;
+    p.Lmax = cache->Lmax;
+    p.W = window < cache->Lmax ? window : cache->Lmax;
+    p.nblk = (cache->Lmax + cache->block - 1) / cache->block;
+    p.block_units = cache->block / logo::kDec8Stage;
+    p.scale_log2 = sl2;
+    p.timeout_ns = 1000000000ull;  // 1 s per wait: far above any legitimate stall
+    NvtxRange range("logo decode, 8-bit cache");
+    cudaError_t e = logo::launch_decode8(p, cache->type, cache->d, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LOGO_OK : cuda_fail(e, "decode launch");
 }
 
