@@ -237,13 +237,17 @@ def test_every_position_belongs_to_one_share_and_every_share_to_one_slot(seed):
     T = sum(units) * Hkv
     if T == 0:
         return
-    N = min((T + 1) // 2, most)
+    least = int(rng.choice([1, 2, 4]))
+    N = min(-(-T // least), most)
+    each, rest = T // N, T % N
+    first = lambda w: w * each + min(w, rest)  # noqa: E731
     owner = {}
     for w in range(N):
-        for u in range(w * T // N, (w + 1) * T // N):
+        assert first(w) < first(w + 1)
+        for u in range(first(w), first(w + 1)):
             owner[u] = w
-            assert ((u + 1) * N - 1) // T == w
-    assert len(owner) == T
+            assert w == (u // (each + 1) if u < rest * (each + 1) else rest + (u - rest * (each + 1)) // each)
+    assert len(owner) == T and first(N) == T
     slots, u = {}, 0
     for pair in range(B * Hkv):
         k = units[pair // Hkv]

@@ -13,10 +13,11 @@
 //   decode8_partial_kernel  one wave of persistent warps.  The work is a list of
 //     units: for every (sequence, key/value head) the 64-position stages before the
 //     window (only where a token is global), then the stages that reach into it.
-//     Warp w takes units [w T / N, (w+1) T / N) of the T, so every warp reads the same
+//     The list is cut into equal shares, one per warp, so every warp reads the same
 //     number of bytes whatever the lengths and gates are; the lengths are read on the
 //     device.  A warp streams its stages through a private ring in shared memory,
-//     filled by TMA (rows swizzled) and tracked by one mbarrier per stage.  Per stage:
+//     filled by TMA (rows swizzled), tracked by one mbarrier per stage and kept full
+//     from one sequence to the next.  Per stage:
 //       S^T = K q^T   mma.sync m16n8k16, fp16 in, fp32 out: positions are the rows,
 //                     the query rows the columns.  Codes become fp16 exactly.  The
 //                     order of the head dimension inside a product is free, so a lane
@@ -62,6 +63,13 @@ namespace {
 #ifndef LOGO_DEC8_STAGES
 #define LOGO_DEC8_STAGES 2
 #endif
+#ifndef LOGO_DEC8_KUNROLL
+#define LOGO_DEC8_KUNROLL 2
+#endif
+#ifndef LOGO_DEC8_KUNROLL
+#define LOGO_DEC8_KUNROLL 2
+#endif
+constexpr int kKUnroll = LOGO_DEC8_KUNROLL;  // of the loop over head-dimension pairs of the scores
 constexpr float kPBias = 15.f;  // P is held times 2^15: the state's m is the maximum less 15
 
 template <int D, int NT>
@@ -91,20 +99,21 @@ struct Plan {
 
 __device__ __forceinline__ bool takes_global(float g, float tau) { return g > tau; }  // false for NaN
 
+// Every load is issued before the first is used: they do not depend on one another.
 __device__ __forceinline__ Plan plan_of(const Decode8Params& p, int b)
 {
     Plan pl{0, 0, 0, 0};
     const int len = p.cache_len[b];
-    if (len <= 0 || len > p.Lmax) return pl;
-    bool any = false;
     const float tau = *p.tau;
-    for (int i = p.n > len ? p.n - len : 0; i < p.n; ++i) any |= takes_global(p.gate[(long long)b * p.n + i], tau);
-    // window edges of the first and last token (32-bit: W <= Lmax and n <= 32)
-    const long long e0 = (long long)len - p.n - p.W + 1, e1 = (long long)len - p.W;
+    bool any = false;
+    for (int i = 0; i < p.n; ++i) any |= takes_global(p.gate[(long long)b * p.n + i], tau) && i >= p.n - len;
+    if (len <= 0 || len > p.Lmax) return pl;
+    // window edges of the first and last token
+    const int e0 = len - p.n - p.W + 1, e1 = len - p.W;
     pl.len = len;
-    pl.in0 = e0 > 0 ? (int)(e0 / kDec8Stage) : 0;
+    pl.in0 = e0 > 0 ? e0 / kDec8Stage : 0;
     pl.in1 = (len + kDec8Stage - 1) / kDec8Stage;
-    pl.out = any && e1 > 0 ? (int)((e1 + kDec8Stage - 1) / kDec8Stage) : 0;
+    pl.out = any && e1 > 0 ? (e1 + kDec8Stage - 1) / kDec8Stage : 0;
     return pl;
 }
 
@@ -119,21 +128,40 @@ __device__ __forceinline__ int warp_scan(int x)  // inclusive
     return x;
 }
 
-// Warps that share T units: at most `most`, each with at least two units.
-__device__ __forceinline__ long long warps_for(long long T, long long most)
-{
-    const long long w = (T + 1) / 2;
-    return w < most ? w : most;
-}
-__device__ __forceinline__ long long first_unit(long long w, long long T, long long N) { return w * T / N; }
-__device__ __forceinline__ long long warp_of(long long u, long long T, long long N) { return ((u + 1) * N - 1) / T; }
+// T units cut into N shares: the first `rest` warps take one unit more than the others.
+// T fits 32 bits: a unit is at least 8 KB of cache, read at most twice.
+struct Shares {
+    int N, each, rest;
+    __device__ __forceinline__ Shares(int T, int most, int least)
+    {
+        const int w = (T + least - 1) / least;  // a share is worth its partial state
+        N = w < most ? w : most;
+        each = N ? T / N : 0;
+        rest = N ? T % N : 0;
+    }
+    __device__ __forceinline__ int first(int w) const { return w * each + (w < rest ? w : rest); }
+    __device__ __forceinline__ int warp_of(int u) const
+    {
+        const int big = rest * (each + 1);
+        return u < big ? u / (each + 1) : rest + (u - big) / each;
+    }
+};
+
+// Fewest units of a share, by the column tiles that a partial state spans.
+__host__ __device__ constexpr int least_units(int nt) { return nt; }
 
 // Partial states: slot (warp + pair) is unique, since along the list either the warp
-// or the pair (sequence, key/value head) moves on from one share to the next.
-template <int D>
-__device__ __forceinline__ float* slot_of(const Decode8Params& p, long long warp, long long pair, int kind)
+// or the pair (sequence, key/value head) moves on from one share to the next.  A slot
+// holds R rows for each kind (0: inside the window, 1: before it): (m, l) and o apart.
+__host__ __device__ inline long long slots8(long long pairs) { return kDec8MaxWarps + pairs; }
+__device__ __forceinline__ long long row_at(const Decode8Params& p, int warp, int pair, int kind)
 {
-    return p.part + (((warp + pair) * 2 + kind) * p.R) * (D + 2);
+    return (((long long)warp + pair) * 2 + kind) * p.R;
+}
+__device__ __forceinline__ float2* part_ml(const Decode8Params& p) { return reinterpret_cast<float2*>(p.part); }
+__device__ __forceinline__ float* part_o(const Decode8Params& p)
+{
+    return p.part + slots8((long long)p.B * p.Hkv) * 2 * p.R * 2;
 }
 
 // ---------------------------------------------------------------- fragments
@@ -197,6 +225,21 @@ __device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
     }
 }
 
+// A word of ldmatrix.trans holds two positions' codes of columns 2g and 2g + 1: bytes
+// (pos 0: 2g, 2g + 1; pos 1: 2g, 2g + 1).  As fp16 pairs over the positions: column 2g, column 2g + 1.
+template <int TYPE>
+__device__ __forceinline__ void to_f16_pairs(uint32_t w, uint32_t& even, uint32_t& odd)
+{
+    if (TYPE == kCacheE4M3) {
+        to_f16<TYPE>(__byte_perm(w, 0u, 0x3120), even, odd);
+    } else {
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(a), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(b), "r"(0x64806480u));
+    }
+}
+
 // Address of the 16-byte unit u of row r in a tile of D-byte rows that TMA wrote with
 // the swizzle of that row length (128B: unit ^ row mod 8; 64B: unit ^ (row / 2) mod 4).
 template <int D>
@@ -234,7 +277,7 @@ struct State8 {
 };
 
 template <int D, int NT>
-__device__ __forceinline__ void store_state8(const State8<D, NT>& st, int R, float* dst)
+__device__ __forceinline__ void store_state8(const Decode8Params& p, const State8<D, NT>& st, long long row)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     #pragma unroll
@@ -245,71 +288,55 @@ __device__ __forceinline__ void store_state8(const State8<D, NT>& st, int R, flo
             #pragma unroll
             for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
             const int r = 8 * nt + 2 * t + c;
-            if (r >= R) continue;
-            float* row = dst + (long long)r * (D + 2);
-            if (g == 0) *reinterpret_cast<float2*>(row) = make_float2(st.m[nt][c], l);
+            if (r >= p.R) continue;
+            if (g == 0) part_ml(p)[row + r] = make_float2(st.m[nt][c], l);
+            float* o = part_o(p) + (row + r) * D + 2 * g;
             #pragma unroll
             for (int u = 0; u < D / 16; ++u)
-                *reinterpret_cast<float2*>(row + 2 + 16 * u + 2 * g) =
-                    make_float2(st.o[u][nt][c], st.o[u][nt][2 + c]);
+                *reinterpret_cast<float2*>(o + 16 * u) = make_float2(st.o[u][nt][c], st.o[u][nt][2 + c]);
         }
     }
 }
 
+// Where in the list a warp is: unit `off` of key/value head hk of sequence b.
+struct Cursor {
+    int b, hk, off, units;
+    Plan pl;
+    __device__ __forceinline__ int pair(int Hkv) const { return b * Hkv + hk; }
+    __device__ __forceinline__ int stage() const { return off < pl.out ? off : off - pl.out + pl.in0; }
+    __device__ __forceinline__ void next_pair(const Decode8Params& p)
+    {
+        off = 0;
+        if (++hk < p.Hkv) return;
+        hk = 0;
+        do {
+            if (++b >= p.B) return;
+            pl = plan_of(p, b);
+        } while (pl.units() == 0);
+        units = pl.units();
+    }
+    __device__ __forceinline__ void next(const Decode8Params& p)
+    {
+        if (++off == units) next_pair(p);
+    }
+};
+
+// The next unit's keys and values into the ring (all lanes keep count, lane 0 copies).
 template <int D, int NT>
-__device__ __forceinline__ void issue_stage(const Decode8Params& p, Ring8& ring, int stage, int slab)
+__device__ __forceinline__ void issue_unit(const Decode8Params& p, Ring8& ring, Cursor& at)
 {
     using G = D8<D, NT>;
-    const uint32_t s = ring.issued % G::kStages;
-    uint8_t* dst = reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(ring.base + s * G::kStageBytes));
-    fence_proxy_async_smem();  // the warp's ldmatrix reads of this stage come before the copy engine's writes
-    mbar_arrive_expect_tx(&ring.full[s], G::kStageBytes);
-    tma_load_3d(dst, &p.tm_k, &ring.full[s], 0, stage * kDec8Stage, slab, policy_evict_first());
-    tma_load_3d(dst + G::kTile, &p.tm_v, &ring.full[s], 0, stage * kDec8Stage, slab, policy_evict_first());
-}
-
-// O^T += V^T P^T over one softmax step (16 MT positions from smem row `row0`), times
-// the V scale.  MASKED: codes at positions whose bit in `vm` is clear count as zero
-// (the cache may hold anything there), and only columns where `cols` says so are
-// added to.
-template <int TYPE, int D, int NT, bool MASKED>
-__device__ __forceinline__ void add_pv(State8<D, NT>& st, uint32_t tileV, int row0, const uint32_t (&pb)[D8<D, NT>::MT][NT][2],
-                                       const float (&al)[NT][2], float vs, const uint32_t* vm, const bool (*cols)[2])
-{
-    constexpr int MT = D8<D, NT>::MT;
-    const int lane = threadIdx.x & 31;
-    #pragma unroll
-    for (int u = 0; u < D / 16; ++u) {
-        float acc[NT][4];
-        #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-        #pragma unroll
-        for (int h = 0; h < MT / 2; ++h) {
-            uint32_t w[4], ev[4], od[4];
-            ldsm4t(swz<D>(tileV, row0 + 32 * h + lane, u), w);
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (MASKED) w[i] &= vm[4 * h + i];
-                // bytes (pos 0: column 2g, 2g+1; pos 1: 2g, 2g+1) -> (2g: pos 0, 1; 2g+1: pos 0, 1)
-                to_f16<TYPE>(__byte_perm(w[i], 0u, 0x3120), ev[i], od[i]);
-            }
-            #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(acc[nt], ev[2 * k], od[2 * k], ev[2 * k + 1], od[2 * k + 1], pb[2 * h + k][nt][0],
-                            pb[2 * h + k][nt][1]);
-        }
-        #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float was = st.o[u][nt][e] * al[nt][e & 1];
-                if (!MASKED || cols[nt][e & 1]) st.o[u][nt][e] = fmaf(acc[nt][e], vs, was);
-            }
+    if ((threadIdx.x & 31) == 0) {
+        const uint32_t s = ring.issued % G::kStages;
+        uint8_t* dst = reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(ring.base + s * G::kStageBytes));
+        const int row = at.stage() * kDec8Stage, slab = at.pair(p.Hkv);
+        fence_proxy_async_smem();  // the warp's reads of this stage come before the copy engine's writes
+        mbar_arrive_expect_tx(&ring.full[s], G::kStageBytes);
+        tma_load_3d(dst, &p.tm_k, &ring.full[s], 0, row, slab, policy_evict_first());
+        tma_load_3d(dst + G::kTile, &p.tm_v, &ring.full[s], 0, row, slab, policy_evict_first());
     }
+    ++ring.issued;
+    at.next(p);
 }
 
 // Per-lane constants of the (sequence, key/value head) at hand.
@@ -319,169 +346,225 @@ struct Rows8 {
     int tok[NT][2];   // the column's token
 };
 
-// Stages [a, e) of slab `slab`.  A column of token i sees positions [lo0 + i, hi0 + i]
-// when `inside`, else [0, hi0 + i]; hi may be negative (nothing seen).  `len` positions
-// of the cache are held.  Returns false when a wait ran out (the CTA aborts).
+// q of one (sequence, key/value head) to fp16 in shared memory, in fragment order: lane
+// (g, t) of unit kk, tile nt holds row 8 nt + g, elements 16 kk + 4t .. + 3.
+template <int D, int NT>
+__device__ __forceinline__ void stage_q(const Decode8Params& p, long long pair, uint2* qs, Rows8<NT>& rw)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint16_t* q = p.q + pair * p.R * D + 4 * t;
+    __syncwarp();
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + g;
+        uint2 w[D / 16];
+        uint32_t big = 0;
+        #pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+            w[kk] = r < p.R ? *reinterpret_cast<const uint2*>(q + (long long)r * D + 16 * kk) : make_uint2(0u, 0u);
+        #pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+            big = __vmaxu2(big, __vmaxu2(w[kk].x & 0x7fff7fffu, w[kk].y & 0x7fff7fffu));
+        big = max(big & 0xffffu, big >> 16);
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        int ex = 141 - (int)(big >> 7);  // largest element into [2^14, 2^15)
+        ex = ex > 127 ? 127 : ex;
+        const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+        #pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint2 f;
+            f.x = pack_f16x2(__uint_as_float(w[kk].x << 16) * up, __uint_as_float(w[kk].x & 0xffff0000u) * up);
+            f.y = pack_f16x2(__uint_as_float(w[kk].y << 16) * up, __uint_as_float(w[kk].y & 0xffff0000u) * up);
+            qs[(kk * NT + nt) * 32 + lane] = f;
+        }
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int e2 = __shfl_sync(0xffffffffu, ex, 4 * (2 * t + c));
+            rw.qf[nt][c] = ldexpf(p.scale_log2, -e2);
+            rw.tok[nt][c] = (8 * nt + 2 * t + c) % p.n;
+        }
+    }
+    __syncwarp();
+}
+
+// A stage that some column sees in part (positions pos0 .., token i sees [lo0 + i, hi0 + i],
+// from 0 on where that is negative): values at positions that no column sees are made
+// zero in shared memory, whatever the cache holds there (their P is zero, but zero times
+// NaN is not).  Says whether an e4m3 NaN is left at a position that only some tokens see.
+template <int TYPE, int D>
+__device__ __noinline__ bool mask_values(uint32_t tileV, int pos0, int lo0, int hi0, int n)
+{
+    const int lane = threadIdx.x & 31;
+    uint8_t* v = reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(tileV));
+    const int last = hi0 + n - 1;
+    bool nan = false;
+    #pragma unroll 1
+    for (int k = lane; k < kDec8Stage * D / 16; k += 32) {
+        const int pos = pos0 + k / (D / 16);
+        uint4* at = reinterpret_cast<uint4*>(v + 16 * k);
+        if (pos < lo0 || pos > last) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+        } else if (TYPE == kCacheE4M3 && (pos < lo0 + n - 1 || pos > hi0)) {
+            const uint4 w = *at;
+            auto has = [](uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u; };
+            nan |= has(w.x) || has(w.y) || has(w.z) || has(w.w);
+        }
+    }
+    __syncwarp();
+    return __any_sync(0xffffffffu, nan);
+}
+
+// Such NaN codes go straight into the output of the tokens that see them, and are made zero.
+template <int D, int NT>
+__device__ __forceinline__ void place_nan(uint32_t tileV, int pos0, int lo0, int hi0, int n, const Rows8<NT>& rw,
+                                          State8<D, NT>& st)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    uint8_t* v = reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(tileV));
+    #pragma unroll 1
+    for (int r = 0; r < kDec8Stage; ++r) {
+        const int pos = pos0 + r;
+        if (pos < lo0 || pos > hi0 + n - 1 || (pos >= lo0 + n - 1 && pos <= hi0)) continue;  // seen by none or by all
+        #pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+            uint16_t* at = reinterpret_cast<uint16_t*>(v + (swz<D>(tileV, r, u) - tileV) + 2 * g);
+            const uint32_t w = *at;
+            const bool nan0 = (w & 0x7fu) == 0x7fu, nan1 = (w & 0x7f00u) == 0x7f00u;
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                #pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const bool sees = pos >= lo0 + rw.tok[nt][c] && pos <= hi0 + rw.tok[nt][c];
+                    if (sees && nan0) st.o[u][nt][c] = __int_as_float(0x7fffffff);
+                    if (sees && nan1) st.o[u][nt][2 + c] = __int_as_float(0x7fffffff);
+                }
+            __syncwarp();  // four lanes share a word
+            *at = (uint16_t)((nan0 ? 0u : w & 0xffu) | (nan1 ? 0u : w & 0xff00u));
+        }
+    }
+    __syncwarp();
+}
+
+// One stage: scores, softmax step, products.  `masked`: some column sees it in part.
 template <int TYPE, int D, int NT>
-__device__ __forceinline__ bool run_stages(const Decode8Params& p, Ring8& ring, State8<D, NT>& st, const Rows8<NT>& rw,
-                                           const uint2* qs, int a, int e, int slab, bool inside, int lo0, int hi0, int len,
-                                           volatile int* abort_flag)
+__device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw, const uint2* qs, uint32_t tileK,
+                                         float ks, float vs, bool masked, int pos0, int lo0, int hi0, int n)
 {
     using G = D8<D, NT>;
     constexpr int MT = G::MT, kSteps = 4 / MT;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int cnt = e - a;
-    if (lane == 0)
-        for (int i = 0; i < cnt && i < G::kStages; ++i) {
-            issue_stage<D, NT>(p, ring, a + i, slab);
-            ++ring.issued;
-        }
-    ring.issued = ring.used + (cnt < G::kStages ? cnt : G::kStages);
-    // Scales of 32 stages at a time, one stage per lane.
-    const float* ksp = p.k_scale + (long long)slab * p.nblk;
-    const float* vsp = p.v_scale + (long long)slab * p.nblk;
-    float ks32 = 0.f, vs32 = 0.f;
+    const int lane = threadIdx.x & 31, g = lane >> 2;
     const int kr = (lane & 7) + 8 * ((lane >> 3) & 1), ku = lane >> 4;  // ldmatrix roles: row, 16-byte unit
-    const int lo_max = inside ? max(lo0 + p.n - 1, 0) : 0;              // every column sees [lo_max, hi0]
-    for (int i = 0; i < cnt; ++i) {
-        if ((i & 31) == 0) {
-            const int blk = (a + i + lane) / p.block_units;
-            ks32 = i + lane < cnt ? ksp[blk] : 0.f;
-            vs32 = i + lane < cnt ? vsp[blk] : 0.f;
-        }
-        const float ks = __shfl_sync(0xffffffffu, ks32, i & 31), vs = __shfl_sync(0xffffffffu, vs32, i & 31);
-        const uint32_t s = ring.used % G::kStages;
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[s], (ring.used / G::kStages) & 1, abort_flag, p.status,
-                                                          p.timeout_ns));
-        if (!ok) return false;
-        const uint32_t tileK = ring.base + s * G::kStageBytes, tileV = tileK + G::kTile;
-        const int pos0 = (a + i) * kDec8Stage;
-        const bool masked = pos0 < lo_max || pos0 + kDec8Stage - 1 > hi0;
+    const uint32_t tileV = tileK + G::kTile;
+    if (masked && mask_values<TYPE, D>(tileV, pos0, lo0, hi0, n) && TYPE == kCacheE4M3)
+        place_nan<D, NT>(tileV, pos0, lo0, hi0, n, rw, st);
+    #pragma unroll 1
+    for (int step = 0; step < kSteps; ++step) {
+        const int row0 = step * 16 * MT;
+        // S^T = K q^T: rows = positions 16 mt + g (+ 8), columns = query rows
+        float sc[MT][NT][4];
         #pragma unroll
-        for (int step = 0; step < kSteps; ++step) {
-            const int row0 = step * 16 * MT;
-            // S^T = K q^T: rows = positions 16 mt + g (+ 8), columns = query rows
-            float sc[MT][NT][4];
+        for (int mt = 0; mt < MT; ++mt)
             #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
                 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    #pragma unroll
-                    for (int x = 0; x < 4; ++x) sc[mt][nt][x] = 0.f;
-            #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
-                uint2 b0[NT], b1[NT];
-                #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    b0[nt] = qs[((2 * kk) * NT + nt) * 32 + lane];
-                    b1[nt] = qs[((2 * kk + 1) * NT + nt) * 32 + lane];
-                }
-                #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t w[4], x[4], y[4];
-                    ldsm4(swz<D>(tileK, row0 + 16 * mt + kr, 2 * kk + ku), w);
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) to_f16<TYPE>(w[q], x[q], y[q]);
-                    #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(sc[mt][nt], x[0], x[1], y[0], y[1], b0[nt].x, b0[nt].y);
-                        mma_f16(sc[mt][nt], x[2], x[3], y[2], y[3], b1[nt].x, b1[nt].y);
-                    }
-                }
-            }
-            // online softmax
-            uint32_t pb[MT][NT][2];
-            float al[NT][2];
+                for (int x = 0; x < 4; ++x) sc[mt][nt][x] = 0.f;
+        #pragma unroll kKUnroll
+        for (int kk = 0; kk < D / 32; ++kk) {
+            uint2 b0[NT], b1[NT];
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                b0[nt] = qs[((2 * kk) * NT + nt) * 32 + lane];
+                b1[nt] = qs[((2 * kk + 1) * NT + nt) * 32 + lane];
+            }
+            #pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                uint32_t w[4], x[4], y[4];
+                ldsm4(swz<D>(tileK, row0 + 16 * mt + kr, 2 * kk + ku), w);
                 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float f = ks * rw.qf[nt][c];
-                    float mx = -INFINITY;
-                    #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float x = sc[mt][nt][2 * h + c] * f;
-                            if (masked) {
-                                const int pos = pos0 + row0 + 16 * mt + 8 * h + g, i0 = rw.tok[nt][c];
-                                if ((inside && pos < lo0 + i0) || pos > hi0 + i0) x = -INFINITY;
-                            }
-                            sc[mt][nt][2 * h + c] = x;
-                            mx = fmaxf(mx, x);
-                        }
-                    #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    const float mn = fmaxf(st.m[nt][c], mx - kPBias);
-                    const float r = mn == -INFINITY ? 0.f : mn;
-                    al[nt][c] = fast_exp2(st.m[nt][c] - r);  // 0 while nothing was seen
-                    st.m[nt][c] = mn;
-                    float sum = 0.f;
-                    #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float x = fast_exp2(sc[mt][nt][2 * h + c] - r);
-                            sc[mt][nt][2 * h + c] = x;
-                            sum += x;
-                        }
-                    st.l[nt][c] = fmaf(st.l[nt][c], al[nt][c], sum);
+                for (int q = 0; q < 4; ++q) to_f16<TYPE>(w[q], x[q], y[q]);
+                #pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(sc[mt][nt], x[0], x[1], y[0], y[1], b0[nt].x, b0[nt].y);
+                    mma_f16(sc[mt][nt], x[2], x[3], y[2], y[3], b1[nt].x, b1[nt].y);
                 }
-                // P^T fragments: the score fragment's 8x8 quarters transposed in registers
+            }
+        }
+        // online softmax
+        uint32_t pb[MT][NT][2];
+        float al[NT][2];
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            #pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float f = ks * rw.qf[nt][c];
                 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        pb[mt][nt][h] = movm(pack_f16x2(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]));
-            }
-            if (!masked) {
-                add_pv<TYPE, D, NT, false>(st, tileV, row0, pb, al, vs, nullptr, nullptr);
-                continue;
-            }
-            // A stage that some column sees in part.  Codes that no column sees are taken as
-            // zero.  With several tokens a code may be NaN at a position that only some of
-            // them see: then one product per token, over that token's positions.
-            const int first = inside ? lo0 : 0, last = hi0 + p.n - 1;
-            uint32_t vm[2 * MT];
-            bool cols[NT][2];
-            auto set_mask = [&](int lo, int hi) {
-                #pragma unroll
-                for (int k = 0; k < 2 * MT; ++k) {
-                    const int q = pos0 + row0 + 8 * k + 2 * t;
-                    vm[k] = (q >= lo && q <= hi ? 0x0000ffffu : 0u) | (q + 1 >= lo && q + 1 <= hi ? 0xffff0000u : 0u);
-                }
-            };
-            bool nan = false;
-            if (TYPE == kCacheE4M3 && p.n > 1) {
-                for (int k = lane; k < 16 * MT * D / 16; k += 32) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(
-                        __cvta_shared_to_generic(tileV + row0 * D + 16 * k));
-                    nan |= (__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                            __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0u;
-                }
-                nan = __any_sync(0xffffffffu, nan);
-            }
-            const int passes = nan ? p.n : 1;
-            for (int i0 = 0; i0 < passes; ++i0) {
-                if (passes == 1)
-                    set_mask(first, last < len - 1 ? last : len - 1);
-                else
-                    set_mask(inside ? lo0 + i0 : 0, hi0 + i0);
-                #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int h = 0; h < 2; ++h) sc[mt][nt][2 * h + c] *= f;
+                if (masked) {
+                    const int lo = lo0 + rw.tok[nt][c] - pos0 - row0 - g, hi = hi0 + rw.tok[nt][c] - pos0 - row0 - g;
                     #pragma unroll
-                    for (int c = 0; c < 2; ++c) cols[nt][c] = passes == 1 || rw.tok[nt][c] == i0;
-                add_pv<TYPE, D, NT, true>(st, tileV, row0, pb, al, vs, vm, cols);
+                    for (int mt = 0; mt < MT; ++mt)
+                        #pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (16 * mt + 8 * h < lo || 16 * mt + 8 * h > hi) sc[mt][nt][2 * h + c] = -INFINITY;
+                }
+                float mx = -INFINITY;
+                #pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mx = fmax3(mx, sc[mt][nt][c], sc[mt][nt][2 + c]);
+                #pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                const float mn = fmaxf(st.m[nt][c], mx - kPBias);
+                const float r = mn == -INFINITY ? 0.f : mn;
+                al[nt][c] = fast_exp2(st.m[nt][c] - r);  // 0 while nothing was seen
+                st.m[nt][c] = mn;
+                float sum = 0.f;
+                #pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float x = fast_exp2(sc[mt][nt][2 * h + c] - r);
+                        sc[mt][nt][2 * h + c] = x;
+                        sum += x;
+                    }
+                st.l[nt][c] = fmaf(st.l[nt][c], al[nt][c], sum);
             }
+            // P^T fragments: the score fragment's 8x8 quarters transposed in registers
+            #pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                #pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    pb[mt][nt][h] = movm(pack_f16x2(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]));
         }
-        ++ring.used;
-        __syncwarp();
-        if (i + G::kStages < cnt) {
-            if (lane == 0) issue_stage<D, NT>(p, ring, a + i + G::kStages, slab);
-            ++ring.issued;
+        // O^T = O^T alpha + (V^T P^T) vs
+        #pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+            float acc[NT][4];
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+            #pragma unroll
+            for (int h = 0; h < MT / 2; ++h) {
+                uint32_t w[4], ev[4], od[4];
+                ldsm4t(swz<D>(tileV, row0 + 32 * h + lane, u), w);
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) to_f16_pairs<TYPE>(w[i], ev[i], od[i]);
+                #pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    #pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(acc[nt], ev[2 * k], od[2 * k], ev[2 * k + 1], od[2 * k + 1], pb[2 * h + k][nt][0],
+                                pb[2 * h + k][nt][1]);
+            }
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    st.o[u][nt][e] = fmaf(acc[nt][e], vs, st.o[u][nt][e] * al[nt][e & 1]);
         }
     }
-    return true;
 }
 
 template <int TYPE, int D, int NT>
@@ -491,117 +574,114 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
     extern __shared__ uint8_t dsmem8[];
     __shared__ uint64_t full_bars[G::kWarps][G::kStages];
     __shared__ int abort_word;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Let the combine kernel's CTAs be placed; they wait for this grid's end before they read.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) abort_word = (*reinterpret_cast<volatile uint32_t*>(p.status) & kStatusTimeout) ? 1 : 0;
+    const uint32_t was = *reinterpret_cast<volatile uint32_t*>(p.status);
     if (lane == 0) {
         for (int s = 0; s < G::kStages; ++s) mbar_init(&full_bars[warp][s], 1);
         fence_barrier_init();
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
     }
+    // The whole list's length (every warp for itself).
+    int T = 0;
+    bool bad = false;
+    for (int b = lane; b - lane < p.B; b += 32) {
+        Plan pl{0, 0, 0, 0};
+        if (b < p.B) {
+            pl = plan_of(p, b);
+            bad |= pl.len == 0 && p.cache_len[b] != 0;
+        }
+        T += (int)__reduce_add_sync(0xffffffffu, pl.units()) * p.Hkv;
+    }
+    if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.status, kStatusBadArgument);
+    if (threadIdx.x == 0) abort_word = (was & kStatusTimeout) ? 1 : 0;
     __syncthreads();
     volatile int* abort_flag = &abort_word;
     if (*abort_flag) return;
+    const Shares sh(T, (int)gridDim.x * G::kWarps, least_units(NT));
+    const int gw = warp * (int)gridDim.x + (int)blockIdx.x;  // few shares: one per SM first
+    if (gw >= sh.N) return;
+    int left = sh.first(gw + 1) - sh.first(gw);
+    Cursor at{};
+    {
+        int before = sh.first(gw);  // units ahead of the share, less those of the sequences passed
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const Plan mine = b0 + lane < p.B ? plan_of(p, b0 + lane) : Plan{0, 0, 0, 0};
+            const int incl = warp_scan(mine.units()) * p.Hkv;
+            const unsigned past = __ballot_sync(0xffffffffu, incl > before);
+            if (past == 0) {
+                before -= __shfl_sync(0xffffffffu, incl, 31);
+                continue;
+            }
+            const int src = __ffs(past) - 1;
+            at.b = b0 + src;
+            at.pl.len = __shfl_sync(0xffffffffu, mine.len, src);
+            at.pl.out = __shfl_sync(0xffffffffu, mine.out, src);
+            at.pl.in0 = __shfl_sync(0xffffffffu, mine.in0, src);
+            at.pl.in1 = __shfl_sync(0xffffffffu, mine.in1, src);
+            at.units = at.pl.units();
+            before -= __shfl_sync(0xffffffffu, incl, src) - at.units * p.Hkv;
+            at.hk = before / at.units;
+            at.off = before % at.units;
+            break;
+        }
+    }
     const uint32_t base = ((smem_u32(dsmem8) + 1023u) & ~1023u) + warp * G::kWarpBytes;
     uint2* qs = reinterpret_cast<uint2*>(__cvta_shared_to_generic(base + G::kRingBytes));
     Ring8 ring{base, full_bars[warp], 0, 0};
-
-    // The whole list's length, then this warp's share of it.
-    long long T = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        int u = 0;
-        if (b < p.B) {
-            const int len = p.cache_len[b];
-            if ((len < 0 || len > p.Lmax) && blockIdx.x == 0 && warp == 0) atomicOr(p.status, kStatusBadArgument);
-            u = plan_of(p, b).units();
-        }
-        T += (long long)__reduce_add_sync(0xffffffffu, u) * p.Hkv;
-    }
-    if (T == 0) return;
-    const long long N = warps_for(T, (long long)gridDim.x * G::kWarps);
-    const long long gw = (long long)warp * gridDim.x + blockIdx.x;  // few warps: one per SM first
-    if (gw >= N) return;
-    long long u = first_unit(gw, T, N);
-    const long long u_end = first_unit(gw + 1, T, N);
+    Cursor ahead = at;
+    int to_issue = left;
+    for (int i = 0; i < G::kStages && to_issue > 0; ++i, --to_issue) issue_unit<D, NT>(p, ring, ahead);
+    Rows8<NT> rw;
+    State8<D, NT> st;
+    int staged = -1;
     bool ok = true;
-    long long before = 0;  // units of the sequences before this group of 32
-    for (int b0 = 0; b0 < p.B && u < u_end && ok; b0 += 32) {
-        const Plan mine = b0 + lane < p.B ? plan_of(p, b0 + lane) : Plan{0, 0, 0, 0};
-        const int incl = warp_scan(mine.units());
-        const long long group = (long long)__shfl_sync(0xffffffffu, incl, 31) * p.Hkv;
-        while (u < u_end && u < before + group && ok) {
-            const unsigned past = __ballot_sync(0xffffffffu, before + (long long)incl * p.Hkv > u);
-            const int src = __ffs(past) - 1, b = b0 + src;
-            Plan pl;
-            pl.len = __shfl_sync(0xffffffffu, mine.len, src);
-            pl.out = __shfl_sync(0xffffffffu, mine.out, src);
-            pl.in0 = __shfl_sync(0xffffffffu, mine.in0, src);
-            pl.in1 = __shfl_sync(0xffffffffu, mine.in1, src);
-            const int units = pl.units();
-            const long long at = u - before - (long long)(__shfl_sync(0xffffffffu, incl, src) - units) * p.Hkv;
-            const int hk = (int)(at / units), off = (int)(at % units);
-            const int stop = u_end - u < units - off ? off + (int)(u_end - u) : units;  // share [off, stop)
-            u += stop - off;
-            // q in fp16 fragment order: lane (g, t) of unit kk, tile nt holds row 8 nt + g, elements
-            // 16 kk + 4t .. + 3
-            const long long pair = (long long)b * p.Hkv + hk;
-            const uint16_t* q = p.q + pair * p.R * D;
-            Rows8<NT> rw;
-            __syncwarp();
-            #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r = 8 * nt + g;
-                uint2 w[D / 16];
-                uint32_t big = 0;
-                #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    w[kk] = r < p.R ? *reinterpret_cast<const uint2*>(q + (long long)r * D + 16 * kk + 4 * t)
-                                    : make_uint2(0u, 0u);
-                    big = __vmaxu2(big, __vmaxu2(w[kk].x & 0x7fff7fffu, w[kk].y & 0x7fff7fffu));
-                }
-                big = max(big & 0xffffu, big >> 16);
-                big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                int ex = 141 - (int)(big >> 7);  // largest element into [2^14, 2^15)
-                ex = ex > 127 ? 127 : ex;
-                const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-                #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    uint2 f;
-                    f.x = pack_f16x2(__uint_as_float(w[kk].x << 16) * up, __uint_as_float(w[kk].x & 0xffff0000u) * up);
-                    f.y = pack_f16x2(__uint_as_float(w[kk].y << 16) * up, __uint_as_float(w[kk].y & 0xffff0000u) * up);
-                    qs[(kk * NT + nt) * 32 + lane] = f;
-                }
-                #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int e2 = __shfl_sync(0xffffffffu, ex, 4 * (2 * t + c));
-                    rw.qf[nt][c] = ldexpf(p.scale_log2, -e2);
-                    rw.tok[nt][c] = (8 * nt + 2 * t + c) % p.n;
-                }
+    while (left > 0 && ok) {
+        // A run: stages of one pair and one kind, ended by the kind's last stage or the share's.
+        const int pair = at.pair(p.Hkv);
+        const bool inside = at.off >= at.pl.out;
+        const int stage0 = at.stage(), most = (inside ? at.units : at.pl.out) - at.off, cnt = left < most ? left : most;
+        // token i sees [lo0 + i, hi0 + i]: its window, or what lies before it
+        const int lo0 = inside ? at.pl.len - p.n - p.W + 1 : -kDec8MaxRows;  // at most 0 for every token
+        const int hi0 = at.pl.len - p.n - (inside ? 0 : p.W);
+        const float* ksp = p.k_scale + (long long)pair * p.nblk;
+        const float* vsp = p.v_scale + (long long)pair * p.nblk;
+        float ks32 = 0.f, vs32 = 0.f;  // scales of 32 stages, one per lane
+        if (lane < cnt) {
+            ks32 = ksp[(stage0 + lane) / p.block_units];
+            vs32 = vsp[(stage0 + lane) / p.block_units];
+        }
+        if (pair != staged) stage_q<D, NT>(p, pair, qs, rw);
+        staged = pair;
+        st.init();
+        for (int i = 0; i < cnt; ++i) {
+            if ((i & 31) == 0 && i > 0) {
+                const int blk = (stage0 + i + lane) / p.block_units;
+                ks32 = i + lane < cnt ? ksp[blk] : 0.f;
+                vs32 = i + lane < cnt ? vsp[blk] : 0.f;
             }
+            const float ks = __shfl_sync(0xffffffffu, ks32, i & 31), vs = __shfl_sync(0xffffffffu, vs32, i & 31);
+            const uint32_t s = ring.used % G::kStages;
+            ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[s], (ring.used / G::kStages) & 1, abort_flag, p.status,
+                                                   p.timeout_ns));
+            if (!ok) break;
+            const int pos0 = (stage0 + i) * kDec8Stage;
+            const bool masked = pos0 < lo0 + p.n - 1 || pos0 + kDec8Stage - 1 > hi0;
+            do_stage<TYPE, D, NT>(st, rw, qs, ring.base + s * G::kStageBytes, ks, vs, masked, pos0, lo0, hi0, p.n);
+            ++ring.used;
             __syncwarp();
-            const int slab = (int)pair;
-            State8<D, NT> st;
-            if (off < pl.out) {  // before the window: token i sees [0, len - n - W + i]
-                st.init();
-                ok = run_stages<TYPE, D, NT>(p, ring, st, rw, qs, off, stop < pl.out ? stop : pl.out, slab, false, 0,
-                                             pl.len - p.n - p.W, pl.len, abort_flag);
-                if (!ok) break;
-                store_state8<D, NT>(st, p.R, slot_of<D>(p, gw, pair, 1));
-            }
-            if (stop > pl.out) {  // the window: token i sees [len - n - W + 1 + i, len - n + i]
-                const int a = (off > pl.out ? off - pl.out : 0) + pl.in0;
-                st.init();
-                ok = run_stages<TYPE, D, NT>(p, ring, st, rw, qs, a, stop - pl.out + pl.in0, slab, true,
-                                             pl.len - p.n - p.W + 1, pl.len - p.n, pl.len, abort_flag);
-                if (!ok) break;
-                store_state8<D, NT>(st, p.R, slot_of<D>(p, gw, pair, 0));
+            if (to_issue > 0) {
+                issue_unit<D, NT>(p, ring, ahead);
+                --to_issue;
             }
         }
-        before += group;
+        if (!ok) break;
+        store_state8<D, NT>(p, st, row_at(p, gw, pair, inside ? 0 : 1));
+        left -= cnt;
+        at.off += cnt;
+        if (at.off == at.units && left > 0) at.next_pair(p);
     }
     if (!ok && lane == 0) {
         // Let every copy this warp started land before the CTA exits.
@@ -614,79 +694,118 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
 
 // ---------------------------------------------------------------- combine
 
-template <int D>
-__global__ void __launch_bounds__(D) decode8_combine_kernel(const __grid_constant__ Decode8Params p, long long most)
+// One CTA per query row, 1 to 8 warps: each warp joins every so-many-th of the row's
+// partial states, a lane holding D / 32 columns, and the warps' sums meet in shared
+// memory in warp order.
+constexpr int kCombineWarps = 8;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(const __grid_constant__ Decode8Params p, int most)
 {
-    __shared__ float red[D / 32];
+    constexpr int C = D / 32;  // columns per lane
+    __shared__ float red_m[2][kCombineWarps], red_l[2][kCombineWarps], red_o[2][kCombineWarps][D];
     __shared__ Plan s_plan;
-    __shared__ long long s_before, s_T;
-    const int col = threadIdx.x, lane = col & 31;
-    const long long pair = blockIdx.x / p.R;
-    const int r = (int)(blockIdx.x % p.R);
-    const int b = (int)(pair / p.Hkv), hk = (int)(pair % p.Hkv), tok = r % p.n;
-    if (col < 32) {
-        long long T = 0, before = 0;
+    __shared__ int s_before, s_T;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = (int)blockDim.x >> 5;
+    const int pair = (int)(blockIdx.x / (unsigned)p.R), r = (int)(blockIdx.x % (unsigned)p.R);
+    const int b = pair / p.Hkv, hk = pair % p.Hkv, tok = r % p.n;
+    const float gate = p.gate[(long long)b * p.n + tok];
+    const bool sel = takes_global(gate, *p.tau);
+    if (warp == 0) {
+        int T = 0, before = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const Plan pl = b0 + lane < p.B ? plan_of(p, b0 + lane) : Plan{0, 0, 0, 0};
             const int un = pl.units();
-            T += (long long)__reduce_add_sync(0xffffffffu, un) * p.Hkv;
-            before += (long long)__reduce_add_sync(0xffffffffu, b0 + lane < b ? un : 0) * p.Hkv;
+            T += (int)__reduce_add_sync(0xffffffffu, un) * p.Hkv;
+            before += (int)__reduce_add_sync(0xffffffffu, b0 + lane < b ? un : 0) * p.Hkv;
             if (b0 + lane == b) s_plan = pl;
         }
         if (lane == 0) s_T = T, s_before = before;
     }
     __syncthreads();
     const Plan pl = s_plan;
-    const long long T = s_T;
-    const float gate = p.gate[(long long)b * p.n + tok];
-    const bool sel = takes_global(gate, *p.tau);
-    if (p.selected && hk == 0 && r < p.n && col == 0) p.selected[(long long)b * p.n + r] = sel ? 1 : 0;
-    uint16_t* out = p.out + (pair * p.R + r) * D;
+    if (p.selected && hk == 0 && r < p.n && tid == 0) p.selected[(long long)b * p.n + r] = sel ? 1 : 0;
+    uint16_t* out = p.out + ((long long)pair * p.R + r) * D;
     if (pl.len < p.n - tok) {  // the token lies before the sequence's start (or the length is invalid)
-        out[col] = 0;
+        for (int c = tid; c < D; c += (int)blockDim.x) out[c] = 0;
         return;
     }
-    const long long N = warps_for(T, most);
-    const long long u0 = s_before + (long long)hk * pl.units();
+    const Shares sh(s_T, most, least_units(NT));
+    const int u0 = s_before + hk * pl.units();
+    // slots of the states inside the window (kind 0) and, for a global token, before it (kind 1)
+    const int w_in = sh.warp_of(u0 + pl.out), n_in = sh.warp_of(u0 + pl.units() - 1) - w_in + 1;
+    const int w_out = sh.warp_of(u0), n_out = sel && pl.out ? sh.warp_of(u0 + pl.out - 1) - w_out + 1 : 0;
+    const long long at[2] = {row_at(p, w_in, pair, 0) + r, row_at(p, w_out, pair, 1) + r};
+    const int cnt[2] = {n_in, n_out};
+    const float2* ml = part_ml(p);
+    const float* po = part_o(p) + lane * C;
+    const long long step = 2LL * p.R;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // (m, l, o) joined over the warps w0 .. w1 that hold stages of the given kind
-    auto join = [&](int kind, long long a, long long e, float& m, float& l, float& o) {
-        m = -INFINITY, l = 0.f, o = 0.f;
-        if (a >= e) return;
-        const long long w0 = warp_of(u0 + a, T, N), w1 = warp_of(u0 + e - 1, T, N);
-        const float* st = slot_of<D>(p, w0, pair, kind) + (long long)r * (D + 2);
-        const long long step = 2LL * p.R * (D + 2);
-        const int cnt = (int)(w1 - w0 + 1);
+    float m[2], l[2], o[2][C];
+    #pragma unroll
+    for (int k = 0; k < 2; ++k) {
         float mx = -INFINITY;
-        for (int k = col; k < cnt; k += D) mx = fmaxf(mx, st[k * step]);
+        for (int i = tid; i < cnt[k]; i += (int)blockDim.x) mx = fmaxf(mx, ml[at[k] + i * step].x);
         #pragma unroll
         for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        __syncthreads();
-        if (lane == 0) red[col >> 5] = mx;
-        __syncthreads();
-        #pragma unroll
-        for (int w = 0; w < D / 32; ++w) m = fmaxf(m, red[w]);
-        #pragma unroll 8
-        for (int k = 0; k < cnt; ++k) {
-            const float* s = st + k * step;
-            const float f = s[0] == -INFINITY ? 0.f : exp2f(s[0] - m);
-            l = fmaf(f, s[1], l);
-            o = fmaf(f, s[2 + col], o);
-        }
-    };
-    float m, l, o;
-    join(0, pl.out, pl.units(), m, l, o);
-    float val = l == 0.f ? 0.f : o / l;
-    if (sel) {
-        float m1, l1, o1;
-        join(1, 0, pl.out, m1, l1, o1);
-        const float M = fmaxf(m, m1);
-        const float f0 = m == -INFINITY ? 0.f : exp2f(m - M), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
-        const float lt = fmaf(f0, l, f1 * l1), ot = fmaf(f0, o, f1 * o1);
-        val = fmaf(1.f / (1.f + expf(-gate)), lt == 0.f ? 0.f : ot / lt, val);
+        if (lane == 0) red_m[k][warp] = mx;
     }
-    const __nv_bfloat16 y = __float2bfloat16_rn(val);
-    out[col] = *reinterpret_cast<const uint16_t*>(&y);
+    __syncthreads();
+    #pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        m[k] = -INFINITY;
+        for (int w = 0; w < nw; ++w) m[k] = fmaxf(m[k], red_m[k][w]);
+        l[k] = 0.f;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) o[k][c] = 0.f;
+        #pragma unroll 4
+        for (int i = warp; i < cnt[k]; i += nw) {
+            const long long row = at[k] + i * step;
+            const float2 s = ml[row];
+            float v[C];
+            if (C == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(po + row * D);
+                v[0] = x.x, v[1] = x.y, v[C - 2] = x.z, v[C - 1] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2*>(po + row * D);
+                v[0] = x.x, v[1] = x.y;
+            }
+            const float f = s.x == -INFINITY ? 0.f : exp2f(s.x - m[k]);
+            l[k] = fmaf(f, s.y, l[k]);
+            #pragma unroll
+            for (int c = 0; c < C; ++c) o[k][c] = fmaf(f, v[c], o[k][c]);
+        }
+    }
+    if (nw > 1) {
+        #pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (lane == 0) red_l[k][warp] = l[k];
+            #pragma unroll
+            for (int c = 0; c < C; ++c) red_o[k][warp][lane * C + c] = o[k][c];
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        #pragma unroll
+        for (int k = 0; k < 2; ++k)
+            for (int w = 1; w < nw; ++w) {
+                l[k] += red_l[k][w];
+                #pragma unroll
+                for (int c = 0; c < C; ++c) o[k][c] += red_o[k][w][lane * C + c];
+            }
+    }
+    float val[C];
+    #pragma unroll
+    for (int c = 0; c < C; ++c) val[c] = l[0] == 0.f ? 0.f : o[0][c] / l[0];
+    if (sel) {
+        const float M = fmaxf(m[0], m[1]);
+        const float f0 = m[0] == -INFINITY ? 0.f : exp2f(m[0] - M), f1 = m[1] == -INFINITY ? 0.f : exp2f(m[1] - M);
+        const float lt = fmaf(f0, l[0], f1 * l[1]), share = 1.f / (1.f + expf(-gate));
+        #pragma unroll
+        for (int c = 0; c < C; ++c) val[c] = fmaf(share, lt == 0.f ? 0.f : fmaf(f0, o[0][c], f1 * o[1][c]) / lt, val[c]);
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(out + lane * C);
+    #pragma unroll
+    for (int c = 0; c < C / 2; ++c) dst[c] = pack_bf16x2(val[2 * c], val[2 * c + 1]);
 }
 
 // CTAs of one wave on the current device (0 until asked), per kernel and device.
@@ -719,16 +838,19 @@ cudaError_t launch_tdn(const Decode8Params& p, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     decode8_partial_kernel<TYPE, D, NT><<<grid, D8<D, NT>::kThreads, D8<D, NT>::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // Warps per row: about four states for each, by the most that a row can have.
+    const long long states = ((long long)grid * D8<D, NT>::kWarps) / ((long long)p.B * p.Hkv) + 2;
+    const int warps = states <= 4 ? 1 : states <= 8 ? 2 : states <= 16 ? 4 : kCombineWarps;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.R));
-    cfg.blockDim = dim3(D);
+    cfg.blockDim = dim3(32 * warps);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode8_combine_kernel<D>, p, (long long)grid * D8<D, NT>::kWarps);
+    return cudaLaunchKernelEx(&cfg, decode8_combine_kernel<D, NT>, p, grid * D8<D, NT>::kWarps);
 }
 
 template <int TYPE, int D>
@@ -742,7 +864,7 @@ cudaError_t launch_td(const Decode8Params& p, cudaStream_t stream)
 
 size_t decode8_partials_bytes(int B, int Hkv, int R, int d)
 {
-    return ((size_t)kDec8MaxWarps + (size_t)B * Hkv) * 2 * R * (d + 2) * sizeof(float);
+    return (size_t)slots8((long long)B * Hkv) * 2 * R * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode8(const Decode8Params& p, int type, int d, cudaStream_t stream)
