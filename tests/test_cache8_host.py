@@ -14,6 +14,7 @@ import torch
 import token_level_dynamic_seq_b200 as logo
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+STAGE = 32   # positions of a unit of work
 FAKE, FAKE2 = ctypes.c_void_p(1 << 20), ctypes.c_void_p(2 << 20)
 no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(),
                                  reason="placeholder pointers are only passed where no GPU exists")
@@ -112,7 +113,7 @@ def test_workspace_size():
     size = lambda c, Hq, n: lib.logo_decode8_workspace_size(by(c), Hq, n)  # noqa: E731
     one = size(desc(k=None), 8, 1)      # the buffers need not exist yet
     assert one > 256 and size(desc(), 8, 4) > one and size(desc(), 16, 1) > one
-    assert one == 256 + (1184 + 4) * 2 * 4 * 130 * 4
+    assert one == 256 + (1776 + 4) * 2 * 4 * 130 * 4
     for c, Hq, n in ((None, 8, 1), (desc(d=32), 8, 1), (desc(), 0, 1), (desc(), 8, 0), (desc(), 8, 9), (desc(), 5, 1)):
         assert size(c, Hq, n) == 0
 
@@ -213,16 +214,18 @@ def plan(length, n, W, any_global, Lmax):
     if length <= 0 or length > Lmax:
         return 0, 0, 0
     e0, e1 = length - n - W + 1, length - W
-    return (-(-e1 // 64) if any_global and e1 > 0 else 0), (e0 // 64 if e0 > 0 else 0), -(-length // 64)
+    return (-(-e1 // STAGE) if any_global and e1 > 0 else 0), (e0 // STAGE if e0 > 0 else 0), -(-length // STAGE)
 
 
 @pytest.mark.parametrize("seed", range(40))
-def test_every_position_belongs_to_one_share_and_every_share_to_one_slot(seed):
+def test_every_unit_of_work_reaches_the_joining_kernel_once(seed):
+    """A model of the list of units, of its shares, of the states that warps and CTAs write and of the slots that the
+    joining kernel reads: each unit's positions are counted once, and no two states share a slot."""
     rng = np.random.default_rng(seed)
     B, Hkv, n = int(rng.integers(1, 70)), int(rng.integers(1, 9)), int(rng.integers(1, 9))
     Lmax = int(rng.integers(1, 5000))
     W = min(int(rng.integers(1, 6000)), Lmax)
-    most = int(rng.choice([5, 148, 740, 888]))
+    grid, warps = int(rng.choice([1, 5, 20, 148])), int(rng.choice([1, 3, 8, 12]))
     lens = rng.integers(0, Lmax + 1, B)
     plans = [plan(int(L), n, W, bool(rng.integers(0, 2)), Lmax) for L in lens]
     units = [o + b - a for o, a, b in plans]
@@ -231,27 +234,69 @@ def test_every_position_belongs_to_one_share_and_every_share_to_one_slot(seed):
         for i in range(max(0, n - L), n):
             t = L - n + i
             first = max(0, t - W + 1)
-            assert a * 64 <= first and (t < b * 64)
+            assert a * STAGE <= first and (t < b * STAGE)
             if o:
-                assert first == 0 or first - 1 < o * 64
+                assert first == 0 or first - 1 < o * STAGE
     T = sum(units) * Hkv
     if T == 0:
         return
-    least = int(rng.choice([1, 2, 4]))
-    N = min(-(-T // least), most)
-    each, rest = T // N, T % N
-    first = lambda w: w * each + min(w, rest)  # noqa: E731
-    owner = {}
-    for w in range(N):
-        assert first(w) < first(w + 1)
-        for u in range(first(w), first(w + 1)):
-            owner[u] = w
-            assert w == (u // (each + 1) if u < rest * (each + 1) else rest + (u - rest * (each + 1)) // each)
-    assert len(owner) == T and first(N) == T
-    slots, u = {}, 0
+    cut = lambda u, most: (min(u, most), u)  # noqa: E731
+
+    def first(share, w):
+        n, u = share
+        return w * (u // n) + min(w, u % n)
+
+    def of(share, x):
+        n, u = share
+        each, rest = u // n, u % n
+        return x // (each + 1) if x < rest * (each + 1) else rest + (x - rest * (each + 1)) // each
+
+    ctas = cut(T, grid)
+    run_of, u = [], 0                       # the list: one run after the other
+    runs = {}
     for pair in range(B * Hkv):
-        k = units[pair // Hkv]
-        for w in {owner[x] for x in range(u, u + k)}:
-            assert slots.setdefault(w + pair, (w, pair)) == (w, pair)
-            assert w + pair < 1184 + B * Hkv
-        u += k
+        o, a, b = plans[pair // Hkv]
+        for kind, n_units in ((1, o), (0, b - a)):
+            if n_units:
+                runs[(pair, kind)] = (u, u + n_units)
+                run_of += [(pair, kind)] * n_units
+                u += n_units
+    assert u == T
+    written = {}                            # slot -> units whose states meet there
+    for c in range(ctas[0]):
+        base = first(ctas, c)
+        size = first(ctas, c + 1) - base
+        assert size > 0
+        inner = cut(size, warps)
+        last = [None] * warps
+        tails = [None] * warps
+        for w in range(inner[0]):
+            mine = list(range(base + first(inner, w), base + first(inner, w + 1)))
+            assert mine and all(of(ctas, x) == c and of(inner, x - base) == w for x in mine)
+            kinds = [run_of[x] for x in mine]
+            last[w] = kinds[-1]
+            tails[w] = [x for x in mine if run_of[x] == kinds[-1]]
+            for key in dict.fromkeys(kinds[:]):
+                if key != kinds[-1]:
+                    slot = (c * warps + w + key[0], key[1])
+                    assert slot not in written
+                    written[slot] = [x for x in mine if run_of[x] == key]
+        w = 0
+        while w < inner[0]:
+            v = w
+            while v + 1 < inner[0] and last[v + 1] == last[w]:
+                v += 1
+            slot = (c * warps + w + last[w][0], last[w][1])
+            assert slot not in written and slot[0] < 1776 + B * Hkv
+            written[slot] = sum(tails[w:v + 1], [])
+            w = v + 1
+    for (pair, kind), (a, e) in runs.items():   # what the joining kernel reads
+        c0, c1 = of(ctas, a), of(ctas, e - 1)
+        share = lambda c: cut(first(ctas, c + 1) - first(ctas, c), warps)  # noqa: E731
+        v0, v1 = of(share(c0), a - first(ctas, c0)), of(share(c1), e - 1 - first(ctas, c1))
+        slots = [c0 * warps + v0] + [c * warps for c in range(c0 + 1, c1 + 1)]
+        if first(share(c1), v1 + 1) != e - first(ctas, c1) and v1 != (v0 if c1 == c0 else 0):
+            slots.append(c1 * warps + v1)
+        got = sum((written.pop((x + pair, kind)) for x in slots), [])
+        assert sorted(got) == list(range(a, e))
+    assert not written

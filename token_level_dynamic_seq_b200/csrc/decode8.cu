@@ -44,6 +44,7 @@
 // largest).  P is 2^15 exp2(s - m) in fp16: 11 bits, 3 more than bf16, with values
 // down to 2^-39 of the largest kept.  The sum l uses the unrounded P.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -57,65 +58,91 @@ namespace logo {
 
 namespace {
 
-#ifndef LOGO_DEC8_WARPS
-#define LOGO_DEC8_WARPS 6
+#ifndef LOGO_DEC8_WARPS1
+#define LOGO_DEC8_WARPS1 8
 #endif
-#ifndef LOGO_DEC8_STAGES
-#define LOGO_DEC8_STAGES 2
+#ifndef LOGO_DEC8_WARPS2
+#define LOGO_DEC8_WARPS2 8
 #endif
-#ifndef LOGO_DEC8_KUNROLL
-#define LOGO_DEC8_KUNROLL 2
+#ifndef LOGO_DEC8_WARPS4
+#define LOGO_DEC8_WARPS4 6
+#endif
+#ifndef LOGO_DEC8_RING
+#define LOGO_DEC8_RING 16384
 #endif
 #ifndef LOGO_DEC8_KUNROLL
 #define LOGO_DEC8_KUNROLL 2
 #endif
 constexpr int kKUnroll = LOGO_DEC8_KUNROLL;  // of the loop over head-dimension pairs of the scores
 constexpr float kPBias = 15.f;  // P is held times 2^15: the state's m is the maximum less 15
+constexpr int kWordsMax = 1024; // sequences whose length and gate decision a CTA keeps in shared memory
 
 template <int D, int NT>
 struct D8 {
     static constexpr int kTile = kDec8Stage * D;                  // codes of K (or V) of one stage, bytes
     static constexpr int kStageBytes = 2 * kTile;                 // K then V
-    static constexpr int kStages = LOGO_DEC8_STAGES * 128 / D;    // ring depth: the same bytes for both D
-    static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kRingBytes = LOGO_DEC8_RING;
+    static constexpr int kStages = kRingBytes / kStageBytes;      // ring depth
     static constexpr int kQBytes = (D / 16) * NT * 32 * 8;        // q fragments of one warp
-    static constexpr int kWarpBytes = kRingBytes + (kQBytes + 1023) / 1024 * 1024;
-    static constexpr int kWarps = NT == 4 ? LOGO_DEC8_WARPS - 1 : LOGO_DEC8_WARPS;  // independent warps per CTA
+    static constexpr int kStateBytes = 8 * NT * (D + 2) * 4;      // partial state, written over the ring at the end
+    static constexpr int kUsedBytes = kRingBytes + kQBytes > kStateBytes ? kRingBytes + kQBytes : kStateBytes;
+    static constexpr int kWarpBytes = (kUsedBytes + 1023) / 1024 * 1024;
+    static constexpr int kWarps = NT == 1 ? LOGO_DEC8_WARPS1 : NT == 2 ? LOGO_DEC8_WARPS2 : LOGO_DEC8_WARPS4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSmem = kWarps * kWarpBytes + 1024;      // + alignment slack
-    static constexpr int MT = NT == 4 ? 2 : 4;                    // 16-position tiles per softmax step
+    static constexpr int MT = kDec8Stage / 16;                    // 16-position tiles of a stage
+    static_assert(kStages >= 2 && kSmem + 6 * 1024 <= 227 * 1024 && kWarps * 148 <= kDec8MaxWarps, "launch shape");
 };
 
 // ---------------------------------------------------------------- the list of units
+
+__device__ __forceinline__ bool takes_global(float g, float tau) { return g > tau; }  // false for NaN
+
+// A sequence's length with the sign bit set where one of its tokens is global; 0 for an
+// empty sequence, kBadLength for one that the cache cannot hold.
+constexpr uint32_t kGlobalBit = 0x80000000u, kBadLength = 0x40000001u;
+
+__device__ __forceinline__ uint32_t word_from(const Decode8Params& p, int b)
+{
+    const int len = p.cache_len[b];
+    const float tau = *p.tau;
+    bool any = false;
+    #pragma unroll 4
+    for (int i = 0; i < p.n; ++i) any |= takes_global(p.gate[(long long)b * p.n + i], tau) && i >= p.n - len;
+    if (len < 0 || len > p.Lmax) return kBadLength;
+    return (uint32_t)len | (any ? kGlobalBit : 0u);
+}
+
+__device__ __noinline__ uint32_t word_far(const Decode8Params& p, int b) { return word_from(p, b); }
+
+// Every thread of the CTA takes part; a barrier has to follow.
+__device__ __forceinline__ void load_words(const Decode8Params& p, uint32_t* words)
+{
+    for (int b = threadIdx.x; b < p.B && b < kWordsMax; b += (int)blockDim.x) words[b] = word_from(p, b);
+}
+__device__ __forceinline__ uint32_t word_of(const Decode8Params& p, const uint32_t* words, int b)
+{
+    return b >= p.B ? 0u : b < kWordsMax ? words[b] : word_far(p, b);
+}
 
 // Units of one sequence: `out` stages before the window ([0, out), sequences with a
 // global token only), then stages [in0, in1).  They overlap in the stages that the
 // first window edges of the n tokens cross.
 struct Plan {
-    int len;   // 0 also for an invalid length
+    int len;  // 0 also for an invalid length
     int out, in0, in1;
-    __device__ int units() const { return out + in1 - in0; }
+    __device__ __forceinline__ Plan() : len(0), out(0), in0(0), in1(0) {}
+    __device__ __forceinline__ Plan(const Decode8Params& p, uint32_t word) : Plan()
+    {
+        if (word == kBadLength) return;
+        len = (int)(word & ~kGlobalBit);
+        const int e0 = len - p.n - p.W + 1, e1 = len - p.W;  // window edges of the first and last token
+        in0 = e0 > 0 ? e0 / kDec8Stage : 0;
+        in1 = (len + kDec8Stage - 1) / kDec8Stage;
+        out = (word & kGlobalBit) && e1 > 0 ? (e1 + kDec8Stage - 1) / kDec8Stage : 0;
+    }
+    __device__ __forceinline__ int units() const { return out + in1 - in0; }
 };
-
-__device__ __forceinline__ bool takes_global(float g, float tau) { return g > tau; }  // false for NaN
-
-// Every load is issued before the first is used: they do not depend on one another.
-__device__ __forceinline__ Plan plan_of(const Decode8Params& p, int b)
-{
-    Plan pl{0, 0, 0, 0};
-    const int len = p.cache_len[b];
-    const float tau = *p.tau;
-    bool any = false;
-    for (int i = 0; i < p.n; ++i) any |= takes_global(p.gate[(long long)b * p.n + i], tau) && i >= p.n - len;
-    if (len <= 0 || len > p.Lmax) return pl;
-    // window edges of the first and last token
-    const int e0 = len - p.n - p.W + 1, e1 = len - p.W;
-    pl.len = len;
-    pl.in0 = e0 > 0 ? e0 / kDec8Stage : 0;
-    pl.in1 = (len + kDec8Stage - 1) / kDec8Stage;
-    pl.out = any && e1 > 0 ? (e1 + kDec8Stage - 1) / kDec8Stage : 0;
-    return pl;
-}
 
 __device__ __forceinline__ int warp_scan(int x)  // inclusive
 {
@@ -128,35 +155,38 @@ __device__ __forceinline__ int warp_scan(int x)  // inclusive
     return x;
 }
 
-// T units cut into N shares: the first `rest` warps take one unit more than the others.
-// T fits 32 bits: a unit is at least 8 KB of cache, read at most twice.
+// T units cut into N shares, at most `most`, none of them empty: the first `rest` shares
+// have one unit more than the others.  T fits 32 bits: a unit is at least 4 KB of
+// cache, read at most twice.
 struct Shares {
     int N, each, rest;
-    __device__ __forceinline__ Shares(int T, int most, int least)
+    __device__ __forceinline__ Shares(int T, int most)
     {
-        const int w = (T + least - 1) / least;  // a share is worth its partial state
-        N = w < most ? w : most;
-        each = N ? T / N : 0;
-        rest = N ? T % N : 0;
+        N = T < most ? T : most;
+        each = N ? (int)((unsigned)T / (unsigned)N) : 0;
+        rest = T - each * N;
     }
     __device__ __forceinline__ int first(int w) const { return w * each + (w < rest ? w : rest); }
-    __device__ __forceinline__ int warp_of(int u) const
+    __device__ __forceinline__ int of(int u) const  // the share that unit u belongs to
     {
-        const int big = rest * (each + 1);
-        return u < big ? u / (each + 1) : rest + (u - big) / each;
+        const bool big = u < rest * (each + 1);
+        const unsigned n = big ? each + 1 : each, x = big ? u : u - rest;
+        return (int)(x / n);  // behind the big shares: rest + (u - rest (each + 1)) / each
     }
 };
 
-// Fewest units of a share, by the column tiles that a partial state spans.
-__host__ __device__ constexpr int least_units(int nt) { return nt; }
-
-// Partial states: slot (warp + pair) is unique, since along the list either the warp
-// or the pair (sequence, key/value head) moves on from one share to the next.  A slot
-// holds R rows for each kind (0: inside the window, 1: before it): (m, l) and o apart.
+// The list is cut into one share per CTA, and that into one per warp.  A run is the
+// stages of one pair (sequence, key/value head) and one kind (0: inside the window, 1:
+// before it).  A warp's last run goes on in the next warp, as a rule: the CTA joins those
+// states and writes one for the run's first warp in the CTA.  A run that ends inside a
+// warp's share is written by that warp alone.
+//
+// Partial states lie in slots of R rows and two kinds, (m, l) and o apart.  Slot (warp of
+// the grid + pair) is unique, since along the list either the warp or the pair moves on.
 __host__ __device__ inline long long slots8(long long pairs) { return kDec8MaxWarps + pairs; }
-__device__ __forceinline__ long long row_at(const Decode8Params& p, int warp, int pair, int kind)
+__device__ __forceinline__ long long row_at(const Decode8Params& p, int gw, int pair, int kind)
 {
-    return (((long long)warp + pair) * 2 + kind) * p.R;
+    return (((long long)gw + pair) * 2 + kind) * p.R;
 }
 __device__ __forceinline__ float2* part_ml(const Decode8Params& p) { return reinterpret_cast<float2*>(p.part); }
 __device__ __forceinline__ float* part_o(const Decode8Params& p)
@@ -205,9 +235,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-// The codes in bytes 0, 1 (-> lo) and 2, 3 (-> hi) of a word as fp16 pairs, exact.
+// Codes as fp16 pairs, exact.  e4m3: the code's value.  int8: (code + 128) 2^-24, a subnormal number whose bits are the code's with the sign bit turned; the
+// products' accumulators start at -128 2^-24 times the other operand's sum instead of zero.
+constexpr uint32_t kOnes = 0x3c003c00u;  // two fp16 ones
+constexpr float kInt8Unit = 16777216.f, kInt8Shift = -128.f / 16777216.f;
+
 template <int TYPE>
-__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)  // bytes 0, 1 and 2, 3
 {
     if (TYPE == kCacheE4M3) {
         asm("{\n\t.reg .b16 x, y;\n\t"
@@ -217,16 +251,15 @@ __device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
             : "=r"(lo), "=r"(hi)
             : "r"(w));
     } else {
-        // 0x6400 | u is 1024 + u in fp16 for u in [0, 255]; u = code + 128
         const uint32_t u = w ^ 0x80808080u;
-        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));  // 1152
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+        lo = __byte_perm(u, 0u, 0x4140);
+        hi = __byte_perm(u, 0u, 0x4342);
     }
 }
 
 // A word of ldmatrix.trans holds two positions' codes of columns 2g and 2g + 1: bytes
-// (pos 0: 2g, 2g + 1; pos 1: 2g, 2g + 1).  As fp16 pairs over the positions: column 2g, column 2g + 1.
+// (pos 0: 2g, 2g + 1; pos 1: 2g, 2g + 1).  As fp16 pairs over the positions: column 2g,
+// column 2g + 1.
 template <int TYPE>
 __device__ __forceinline__ void to_f16_pairs(uint32_t w, uint32_t& even, uint32_t& odd)
 {
@@ -234,9 +267,8 @@ __device__ __forceinline__ void to_f16_pairs(uint32_t w, uint32_t& even, uint32_
         to_f16<TYPE>(__byte_perm(w, 0u, 0x3120), even, odd);
     } else {
         const uint32_t u = w ^ 0x80808080u;
-        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(a), "r"(0x64806480u));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(b), "r"(0x64806480u));
+        even = __byte_perm(u, 0u, 0x4240);
+        odd = __byte_perm(u, 0u, 0x4341);
     }
 }
 
@@ -255,6 +287,12 @@ struct Ring8 {
     uint64_t* full;  // one barrier per stage
     uint32_t issued, used;
 };
+
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status,
+                                       unsigned long long limit_ns)
+{
+    return mbar_wait(bar, parity, abort_flag, status, limit_ns);
+}
 
 // Softmax state of the warp's query rows.  Lane (g, t) = (lane / 4, lane % 4) has
 // columns 8 nt + 2t + c (c = 0, 1): their maxima (shared by the 8 lanes of the same
@@ -276,79 +314,119 @@ struct State8 {
     }
 };
 
+__device__ __forceinline__ void store_if(bool yes, void* at, float a, float b)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t@q st.v2.f32 [%1], {%2, %3};\n\t}" ::"r"((int)yes), "l"(at),
+                 "f"(a), "f"(b)
+                 : "memory");
+}
+
+// The state's rows to (m, l) at ml[r] and o at o[r * D], in shared or global memory.  Predicated
+// stores and no branches: this code runs once or twice in a launch, and every branch of it
+// would wait for its instructions.
 template <int D, int NT>
-__device__ __forceinline__ void store_state8(const Decode8Params& p, const State8<D, NT>& st, long long row)
+__device__ __forceinline__ void store_state8(State8<D, NT>& st, int R, float2* ml, float* o)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int off = 4; off < 32; off <<= 1)
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            #pragma unroll
+            for (int c = 0; c < 2; ++c) st.l[nt][c] += __shfl_xor_sync(0xffffffffu, st.l[nt][c], off);
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            float l = st.l[nt][c];
-            #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
             const int r = 8 * nt + 2 * t + c;
-            if (r >= p.R) continue;
-            if (g == 0) part_ml(p)[row + r] = make_float2(st.m[nt][c], l);
-            float* o = part_o(p) + (row + r) * D + 2 * g;
+            store_if(r < R && g == 0, ml + r, st.m[nt][c], st.l[nt][c]);
+            float* row = o + r * D + 2 * g;
             #pragma unroll
-            for (int u = 0; u < D / 16; ++u)
-                *reinterpret_cast<float2*>(o + 16 * u) = make_float2(st.o[u][nt][c], st.o[u][nt][2 + c]);
+            for (int u = 0; u < D / 16; ++u) store_if(r < R, row + 16 * u, st.o[u][nt][c], st.o[u][nt][2 + c]);
         }
+}
+
+// Joins the states of warps first .. last of the CTA, held in their shared memory (`at`: the
+// first warp's; o, then (m, l)), row by row: this warp takes every so-many-th row.
+template <int D, int NT>
+__device__ __forceinline__ void join_states(const Decode8Params& p, const uint8_t* at, int size, int rank, long long row)
+{
+    constexpr int C = D / 32;
+    const int lane = threadIdx.x & 31;
+    for (int r = rank; r < p.R; r += size) {
+        auto ml = [&](int i) {
+            return reinterpret_cast<const float2*>(at + (long long)i * D8<D, NT>::kWarpBytes + 8 * NT * D * 4)[r];
+        };
+        const float mine = lane < size ? ml(lane).x : -INFINITY;
+        float m = mine;
+        #pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float f_mine = mine == -INFINITY ? 0.f : exp2f(mine - m);
+        float l = 0.f, o[C];
+        #pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = 0.f;
+        #pragma unroll 4
+        for (int i = 0; i < size; ++i) {
+            const float f = __shfl_sync(0xffffffffu, f_mine, i);
+            const float* src = reinterpret_cast<const float*>(at + (long long)i * D8<D, NT>::kWarpBytes) + r * D + lane;
+            l = fmaf(f, ml(i).y, l);
+            #pragma unroll
+            for (int c = 0; c < C; ++c) o[c] = fmaf(f, src[32 * c], o[c]);
+        }
+        if (lane == 0) part_ml(p)[row + r] = make_float2(m, l);
+        float* dst = part_o(p) + (row + r) * D + lane;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) dst[32 * c] = o[c];
     }
 }
 
-// Where in the list a warp is: unit `off` of key/value head hk of sequence b.
+// Where in the list a warp's copies are: unit `off` of key/value head hk of sequence b.
 struct Cursor {
     int b, hk, off, units;
     Plan pl;
-    __device__ __forceinline__ int pair(int Hkv) const { return b * Hkv + hk; }
-    __device__ __forceinline__ int stage() const { return off < pl.out ? off : off - pl.out + pl.in0; }
-    __device__ __forceinline__ void next_pair(const Decode8Params& p)
-    {
-        off = 0;
-        if (++hk < p.Hkv) return;
-        hk = 0;
-        do {
-            if (++b >= p.B) return;
-            pl = plan_of(p, b);
-        } while (pl.units() == 0);
-        units = pl.units();
-    }
-    __device__ __forceinline__ void next(const Decode8Params& p)
-    {
-        if (++off == units) next_pair(p);
-    }
 };
 
-// The next unit's keys and values into the ring (all lanes keep count, lane 0 copies).
+// The next unit's keys and values into the ring (all lanes keep count, lane 0 copies), and
+// beside them what the warp has to know of the stage: the run (2 pair + kind), the stage's
+// index in the sequence and the sequence's length.
 template <int D, int NT>
-__device__ __forceinline__ void issue_unit(const Decode8Params& p, Ring8& ring, Cursor& at)
+__device__ __forceinline__ void issue_unit(const Decode8Params& p, const uint32_t* words, Ring8& ring, int4* units, Cursor& at)
 {
     using G = D8<D, NT>;
+    const bool inside = at.off >= at.pl.out;
+    const int stage = inside ? at.off - at.pl.out + at.pl.in0 : at.off, pair = at.b * p.Hkv + at.hk;
+    const uint32_t s = ring.issued % G::kStages;
     if ((threadIdx.x & 31) == 0) {
-        const uint32_t s = ring.issued % G::kStages;
         uint8_t* dst = reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(ring.base + s * G::kStageBytes));
-        const int row = at.stage() * kDec8Stage, slab = at.pair(p.Hkv);
         fence_proxy_async_smem();  // the warp's reads of this stage come before the copy engine's writes
         mbar_arrive_expect_tx(&ring.full[s], G::kStageBytes);
-        tma_load_3d(dst, &p.tm_k, &ring.full[s], 0, row, slab, policy_evict_first());
-        tma_load_3d(dst + G::kTile, &p.tm_v, &ring.full[s], 0, row, slab, policy_evict_first());
+        tma_load_3d(dst, &p.tm_k, &ring.full[s], 0, stage * kDec8Stage, pair, policy_evict_first());
+        tma_load_3d(dst + G::kTile, &p.tm_v, &ring.full[s], 0, stage * kDec8Stage, pair, policy_evict_first());
+        units[s] = make_int4(2 * pair + (inside ? 0 : 1), stage, at.pl.len, 0);
     }
     ++ring.issued;
-    at.next(p);
+    if (++at.off < at.units) return;
+    at.off = 0;
+    if (++at.hk < p.Hkv) return;
+    at.hk = 0;
+    do {
+        if (++at.b >= p.B) return;
+        at.pl = Plan(p, word_of(p, words, at.b));
+        at.units = at.pl.units();
+    } while (at.units == 0);
 }
 
 // Per-lane constants of the (sequence, key/value head) at hand.
 template <int NT>
 struct Rows8 {
     float qf[NT][2];  // scale * log2(e) / (the power of two in the row's fp16 q)
+    float s0[NT][2];  // what the scores' accumulators start at (int8)
     int tok[NT][2];   // the column's token
 };
 
 // q of one (sequence, key/value head) to fp16 in shared memory, in fragment order: lane
 // (g, t) of unit kk, tile nt holds row 8 nt + g, elements 16 kk + 4t .. + 3.
-template <int D, int NT>
+template <int TYPE, int D, int NT>
 __device__ __forceinline__ void stage_q(const Decode8Params& p, long long pair, uint2* qs, Rows8<NT>& rw)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -369,20 +447,30 @@ __device__ __forceinline__ void stage_q(const Decode8Params& p, long long pair, 
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
         int ex = 141 - (int)(big >> 7);  // largest element into [2^14, 2^15)
-        ex = ex > 127 ? 127 : ex;
+        ex = ex > 126 ? 126 : ex;
         const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+        float sum = 0.f;  // of the row's fp16 values
         #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             uint2 f;
             f.x = pack_f16x2(__uint_as_float(w[kk].x << 16) * up, __uint_as_float(w[kk].x & 0xffff0000u) * up);
             f.y = pack_f16x2(__uint_as_float(w[kk].y << 16) * up, __uint_as_float(w[kk].y & 0xffff0000u) * up);
             qs[(kk * NT + nt) * 32 + lane] = f;
+            if (TYPE == kCacheInt8) {
+                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&f.x));
+                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&f.y));
+                sum += (a.x + a.y) + (b.x + b.y);
+            }
+        }
+        if (TYPE == kCacheInt8) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         }
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int e2 = __shfl_sync(0xffffffffu, ex, 4 * (2 * t + c));
-            rw.qf[nt][c] = ldexpf(p.scale_log2, -e2);
-            rw.tok[nt][c] = (8 * nt + 2 * t + c) % p.n;
+            rw.qf[nt][c] = p.scale_log2 * (TYPE == kCacheInt8 ? kInt8Unit : 1.f) * __uint_as_float((uint32_t)(127 - e2) << 23);
+            rw.s0[nt][c] = TYPE == kCacheInt8 ? kInt8Shift * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + c)) : 0.f;
         }
     }
     __syncwarp();
@@ -452,118 +540,139 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
                                          float ks, float vs, bool masked, int pos0, int lo0, int hi0, int n)
 {
     using G = D8<D, NT>;
-    constexpr int MT = G::MT, kSteps = 4 / MT;
+    constexpr int MT = G::MT;
     const int lane = threadIdx.x & 31, g = lane >> 2;
     const int kr = (lane & 7) + 8 * ((lane >> 3) & 1), ku = lane >> 4;  // ldmatrix roles: row, 16-byte unit
     const uint32_t tileV = tileK + G::kTile;
     if (masked && mask_values<TYPE, D>(tileV, pos0, lo0, hi0, n) && TYPE == kCacheE4M3)
         place_nan<D, NT>(tileV, pos0, lo0, hi0, n, rw, st);
-    #pragma unroll 1
-    for (int step = 0; step < kSteps; ++step) {
-        const int row0 = step * 16 * MT;
-        // S^T = K q^T: rows = positions 16 mt + g (+ 8), columns = query rows
-        float sc[MT][NT][4];
+    // S^T = K q^T: rows = positions 16 mt + g (+ 8), columns = query rows
+    float sc[MT][NT][4];
+    #pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
         #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
             #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                #pragma unroll
-                for (int x = 0; x < 4; ++x) sc[mt][nt][x] = 0.f;
-        #pragma unroll kKUnroll
-        for (int kk = 0; kk < D / 32; ++kk) {
-            uint2 b0[NT], b1[NT];
-            #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                b0[nt] = qs[((2 * kk) * NT + nt) * 32 + lane];
-                b1[nt] = qs[((2 * kk + 1) * NT + nt) * 32 + lane];
-            }
-            #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                uint32_t w[4], x[4], y[4];
-                ldsm4(swz<D>(tileK, row0 + 16 * mt + kr, 2 * kk + ku), w);
-                #pragma unroll
-                for (int q = 0; q < 4; ++q) to_f16<TYPE>(w[q], x[q], y[q]);
-                #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(sc[mt][nt], x[0], x[1], y[0], y[1], b0[nt].x, b0[nt].y);
-                    mma_f16(sc[mt][nt], x[2], x[3], y[2], y[3], b1[nt].x, b1[nt].y);
-                }
-            }
-        }
-        // online softmax
-        uint32_t pb[MT][NT][2];
-        float al[NT][2];
+            for (int x = 0; x < 4; ++x) sc[mt][nt][x] = rw.s0[nt][x & 1];
+    #pragma unroll kKUnroll
+    for (int kk = 0; kk < D / 32; ++kk) {
+        uint2 b0[NT], b1[NT];
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            b0[nt] = qs[((2 * kk) * NT + nt) * 32 + lane];
+            b1[nt] = qs[((2 * kk + 1) * NT + nt) * 32 + lane];
+        }
+        #pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            uint32_t w[4], x[4], y[4];
+            ldsm4(swz<D>(tileK, 16 * mt + kr, 2 * kk + ku), w);
             #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float f = ks * rw.qf[nt][c];
-                #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    #pragma unroll
-                    for (int h = 0; h < 2; ++h) sc[mt][nt][2 * h + c] *= f;
-                if (masked) {
-                    const int lo = lo0 + rw.tok[nt][c] - pos0 - row0 - g, hi = hi0 + rw.tok[nt][c] - pos0 - row0 - g;
-                    #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (16 * mt + 8 * h < lo || 16 * mt + 8 * h > hi) sc[mt][nt][2 * h + c] = -INFINITY;
-                }
-                float mx = -INFINITY;
-                #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mx = fmax3(mx, sc[mt][nt][c], sc[mt][nt][2 + c]);
-                #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float mn = fmaxf(st.m[nt][c], mx - kPBias);
-                const float r = mn == -INFINITY ? 0.f : mn;
-                al[nt][c] = fast_exp2(st.m[nt][c] - r);  // 0 while nothing was seen
-                st.m[nt][c] = mn;
-                float sum = 0.f;
-                #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float x = fast_exp2(sc[mt][nt][2 * h + c] - r);
-                        sc[mt][nt][2 * h + c] = x;
-                        sum += x;
-                    }
-                st.l[nt][c] = fmaf(st.l[nt][c], al[nt][c], sum);
+            for (int q = 0; q < 4; ++q) to_f16<TYPE>(w[q], x[q], y[q]);
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mma_f16(sc[mt][nt], x[0], x[1], y[0], y[1], b0[nt].x, b0[nt].y);
+                mma_f16(sc[mt][nt], x[2], x[3], y[2], y[3], b1[nt].x, b1[nt].y);
             }
-            // P^T fragments: the score fragment's 8x8 quarters transposed in registers
+        }
+    }
+    // online softmax
+    uint32_t pb[MT][NT][2];
+    float al[NT][2];
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float f = ks * rw.qf[nt][c];
             #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
                 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    pb[mt][nt][h] = movm(pack_f16x2(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]));
-        }
-        // O^T = O^T alpha + (V^T P^T) vs
-        #pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-            float acc[NT][4];
-            #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int h = 0; h < 2; ++h) sc[mt][nt][2 * h + c] *= f;
+            if (masked) {
+                const int lo = lo0 + rw.tok[nt][c] - pos0 - g, hi = hi0 + rw.tok[nt][c] - pos0 - g;
                 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-            #pragma unroll
-            for (int h = 0; h < MT / 2; ++h) {
-                uint32_t w[4], ev[4], od[4];
-                ldsm4t(swz<D>(tileV, row0 + 32 * h + lane, u), w);
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) to_f16_pairs<TYPE>(w[i], ev[i], od[i]);
-                #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int mt = 0; mt < MT; ++mt)
                     #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16(acc[nt], ev[2 * k], od[2 * k], ev[2 * k + 1], od[2 * k + 1], pb[2 * h + k][nt][0],
-                                pb[2 * h + k][nt][1]);
+                    for (int h = 0; h < 2; ++h)
+                        if (16 * mt + 8 * h < lo || 16 * mt + 8 * h > hi) sc[mt][nt][2 * h + c] = -INFINITY;
             }
+            float mx = -INFINITY;
+            #pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mx = fmax3(mx, sc[mt][nt][c], sc[mt][nt][2 + c]);
+            #pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float mn = fmaxf(st.m[nt][c], mx - kPBias);
+            const float r = mn == -INFINITY ? 0.f : mn;
+            al[nt][c] = fast_exp2(st.m[nt][c] - r);  // 0 while nothing was seen
+            st.m[nt][c] = mn;
+            float sum = 0.f;
+            #pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float x = fast_exp2(sc[mt][nt][2 * h + c] - r);
+                    sc[mt][nt][2 * h + c] = x;
+                    sum += x;
+                }
+            st.l[nt][c] = fmaf(st.l[nt][c], al[nt][c], sum);
+        }
+        // P^T fragments: the score fragment's 8x8 quarters transposed in registers
+        #pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            #pragma unroll
+            for (int h = 0; h < 2; ++h)
+                pb[mt][nt][h] = movm(pack_f16x2(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]));
+    }
+    // O^T = O^T alpha + (V^T P^T) vs; most stages leave every maximum as it is
+    bool moved = false;
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) moved |= al[nt][0] != 1.f || al[nt][1] != 1.f;
+    if (__any_sync(0xffffffffu, moved)) {
+        #pragma unroll
+        for (int u = 0; u < D / 16; ++u)
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    st.o[u][nt][e] = fmaf(acc[nt][e], vs, st.o[u][nt][e] * al[nt][e & 1]);
+                for (int e = 0; e < 4; ++e) st.o[u][nt][e] *= al[nt][e & 1];
+    }
+    float o0[NT][4];  // what the products start at: zero, or (int8) -128 2^-24 sum P
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) o0[nt][e] = 0.f;
+        if (TYPE == kCacheInt8) {
+            #pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                mma_f16(o0[nt], kOnes, kOnes, kOnes, kOnes, pb[mt][nt][0], pb[mt][nt][1]);
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) o0[nt][e] *= kInt8Shift;
         }
+    }
+    if (TYPE == kCacheInt8) vs *= kInt8Unit;
+    #pragma unroll
+    for (int u = 0; u < D / 16; ++u) {
+        float acc[NT][4];
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][e] = o0[nt][e];
+        #pragma unroll
+        for (int h = 0; h < MT / 2; ++h) {
+            uint32_t w[4], ev[4], od[4];
+            ldsm4t(swz<D>(tileV, 32 * h + lane, u), w);
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) to_f16_pairs<TYPE>(w[i], ev[i], od[i]);
+            #pragma unroll
+            for (int k = 0; k < 2; ++k)
+                #pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(acc[nt], ev[2 * k], od[2 * k], ev[2 * k + 1], od[2 * k + 1], pb[2 * h + k][nt][0],
+                            pb[2 * h + k][nt][1]);
+        }
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                st.o[u][nt][e] = fmaf(acc[nt][e], vs, st.o[u][nt][e]);
     }
 }
 
@@ -573,8 +682,11 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
     using G = D8<D, NT>;
     extern __shared__ uint8_t dsmem8[];
     __shared__ uint64_t full_bars[G::kWarps][G::kStages];
+    __shared__ uint32_t words[kWordsMax];
     __shared__ int abort_word;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ int4 unit_info[G::kWarps][G::kStages];
+    __shared__ int last_run[G::kWarps];  // 2 pair + kind of each warp's last run, -1: none
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
     // Let the combine kernel's CTAs be placed; they wait for this grid's end before they read.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t was = *reinterpret_cast<volatile uint32_t*>(p.status);
@@ -584,31 +696,34 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
     }
-    // The whole list's length (every warp for itself).
-    int T = 0;
-    bool bad = false;
-    for (int b = lane; b - lane < p.B; b += 32) {
-        Plan pl{0, 0, 0, 0};
-        if (b < p.B) {
-            pl = plan_of(p, b);
-            bad |= pl.len == 0 && p.cache_len[b] != 0;
-        }
-        T += (int)__reduce_add_sync(0xffffffffu, pl.units()) * p.Hkv;
-    }
-    if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.status, kStatusBadArgument);
+    load_words(p, words);
     if (threadIdx.x == 0) abort_word = (was & kStatusTimeout) ? 1 : 0;
     __syncthreads();
     volatile int* abort_flag = &abort_word;
     if (*abort_flag) return;
-    const Shares sh(T, (int)gridDim.x * G::kWarps, least_units(NT));
-    const int gw = warp * (int)gridDim.x + (int)blockIdx.x;  // few shares: one per SM first
-    if (gw >= sh.N) return;
-    int left = sh.first(gw + 1) - sh.first(gw);
+    // The whole list's length (every warp for itself).
+    int T = 0;
+    bool bad = false;
+    Plan mine;
+    for (int b = lane; b - lane < p.B; b += 32) {
+        const uint32_t w = word_of(p, words, b);
+        bad |= w == kBadLength;
+        mine = Plan(p, w);
+        T += (int)__reduce_add_sync(0xffffffffu, mine.units()) * p.Hkv;
+    }
+    if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.status, kStatusBadArgument);
+    const Shares ctas(T, (int)gridDim.x);
+    const int cta = (int)blockIdx.x;
+    if (cta >= ctas.N) return;
+    const int u_cta = ctas.first(cta);
+    const Shares sh(ctas.first(cta + 1) - u_cta, G::kWarps);
+    const int gw = cta * G::kWarps + warp;
+    int left = warp < sh.N ? sh.first(warp + 1) - sh.first(warp) : 0;
     Cursor at{};
-    {
-        int before = sh.first(gw);  // units ahead of the share, less those of the sequences passed
+    if (left > 0) {
+        int before = u_cta + sh.first(warp);  // units ahead of the share, less those of the sequences passed
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const Plan mine = b0 + lane < p.B ? plan_of(p, b0 + lane) : Plan{0, 0, 0, 0};
+            if (p.B > 32) mine = Plan(p, word_of(p, words, b0 + lane));
             const int incl = warp_scan(mine.units()) * p.Hkv;
             const unsigned past = __ballot_sync(0xffffffffu, incl > before);
             if (past == 0) {
@@ -623,174 +738,236 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
             at.pl.in1 = __shfl_sync(0xffffffffu, mine.in1, src);
             at.units = at.pl.units();
             before -= __shfl_sync(0xffffffffu, incl, src) - at.units * p.Hkv;
-            at.hk = before / at.units;
-            at.off = before % at.units;
+            at.hk = (int)((unsigned)before / (unsigned)at.units);
+            at.off = before - at.hk * at.units;
             break;
         }
     }
     const uint32_t base = ((smem_u32(dsmem8) + 1023u) & ~1023u) + warp * G::kWarpBytes;
     uint2* qs = reinterpret_cast<uint2*>(__cvta_shared_to_generic(base + G::kRingBytes));
     Ring8 ring{base, full_bars[warp], 0, 0};
-    Cursor ahead = at;
-    int to_issue = left;
-    for (int i = 0; i < G::kStages && to_issue > 0; ++i, --to_issue) issue_unit<D, NT>(p, ring, ahead);
-    Rows8<NT> rw;
-    State8<D, NT> st;
-    int staged = -1;
+    int to_issue = left, run = -1, lo0 = 0, hi0 = 0, first = 0, last = 0;
+    float ks32 = 0.f, vs32 = 0.f;  // scales of stages first .. first + 31, one per lane
     bool ok = true;
-    while (left > 0 && ok) {
-        // A run: stages of one pair and one kind, ended by the kind's last stage or the share's.
-        const int pair = at.pair(p.Hkv);
-        const bool inside = at.off >= at.pl.out;
-        const int stage0 = at.stage(), most = (inside ? at.units : at.pl.out) - at.off, cnt = left < most ? left : most;
-        // token i sees [lo0 + i, hi0 + i]: its window, or what lies before it
-        const int lo0 = inside ? at.pl.len - p.n - p.W + 1 : -kDec8MaxRows;  // at most 0 for every token
-        const int hi0 = at.pl.len - p.n - (inside ? 0 : p.W);
-        const float* ksp = p.k_scale + (long long)pair * p.nblk;
-        const float* vsp = p.v_scale + (long long)pair * p.nblk;
-        float ks32 = 0.f, vs32 = 0.f;  // scales of 32 stages, one per lane
-        if (lane < cnt) {
-            ks32 = ksp[(stage0 + lane) / p.block_units];
-            vs32 = vsp[(stage0 + lane) / p.block_units];
+    Rows8<NT> rw;
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int r = 8 * nt + 2 * t + c;
+            rw.tok[nt][c] = r - p.n * (int)((r + 0.5f) / (float)p.n);  // r mod n, both at most 32
         }
-        if (pair != staged) stage_q<D, NT>(p, pair, qs, rw);
-        staged = pair;
-        st.init();
-        for (int i = 0; i < cnt; ++i) {
-            if ((i & 31) == 0 && i > 0) {
-                const int blk = (stage0 + i + lane) / p.block_units;
-                ks32 = i + lane < cnt ? ksp[blk] : 0.f;
-                vs32 = i + lane < cnt ? vsp[blk] : 0.f;
-            }
-            const float ks = __shfl_sync(0xffffffffu, ks32, i & 31), vs = __shfl_sync(0xffffffffu, vs32, i & 31);
-            const uint32_t s = ring.used % G::kStages;
-            ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[s], (ring.used / G::kStages) & 1, abort_flag, p.status,
-                                                   p.timeout_ns));
-            if (!ok) break;
-            const int pos0 = (stage0 + i) * kDec8Stage;
-            const bool masked = pos0 < lo0 + p.n - 1 || pos0 + kDec8Stage - 1 > hi0;
-            do_stage<TYPE, D, NT>(st, rw, qs, ring.base + s * G::kStageBytes, ks, vs, masked, pos0, lo0, hi0, p.n);
-            ++ring.used;
-            __syncwarp();
-            if (to_issue > 0) {
-                issue_unit<D, NT>(p, ring, ahead);
-                --to_issue;
-            }
+    State8<D, NT> st;
+    st.init();
+    for (;;) {
+        while (to_issue > 0 && ring.issued - ring.used < (uint32_t)G::kStages) {
+            issue_unit<D, NT>(p, words, ring, unit_info[warp], at);
+            --to_issue;
         }
+        __syncwarp();
+        const uint32_t s = ring.used % G::kStages;
+        const int4 unit = left > 0 ? unit_info[warp][s] : make_int4(-1, 0, 0, 0);
+        if (unit.x != run || left == 0) {
+            if (left == 0) break;  // the share's last state stays in registers
+            if (run >= 0) {        // a run ends inside the share: its state goes to its slot
+                const long long row = row_at(p, gw, run >> 1, run & 1);
+                store_state8<D, NT>(st, p.R, part_ml(p) + row, part_o(p) + row * D);
+            }
+            // token i sees [lo0 + i, hi0 + i]: its window, or what lies before it (lo0 then at
+            // most 0 for every token)
+            const bool inside = !(unit.x & 1);
+            lo0 = inside ? unit.z - p.n - p.W + 1 : -kDec8MaxRows;
+            hi0 = unit.z - p.n - (inside ? 0 : p.W);
+            first = -64;
+            last = (unit.z - 1) / kDec8Stage;
+            const int pair = unit.x >> 1;
+            if (run < 0 || pair != run >> 1) stage_q<TYPE, D, NT>(p, pair, qs, rw);
+            run = unit.x;
+            st.init();
+        }
+        if (unit.y - first >= 32) {
+            first = unit.y;
+            const int blk = (first + lane < last ? first + lane : last) / p.block_units;
+            ks32 = p.k_scale[(long long)(run >> 1) * p.nblk + blk];
+            vs32 = p.v_scale[(long long)(run >> 1) * p.nblk + blk];
+        }
+        const float ks = __shfl_sync(0xffffffffu, ks32, unit.y - first), vs = __shfl_sync(0xffffffffu, vs32, unit.y - first);
+        const uint32_t parity = (ring.used / G::kStages) & 1;
+        ok = mbar_try_wait(&ring.full[s], parity) || wait_long(&ring.full[s], parity, abort_flag, p.status, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        store_state8<D, NT>(p, st, row_at(p, gw, pair, inside ? 0 : 1));
-        left -= cnt;
-        at.off += cnt;
-        if (at.off == at.units && left > 0) at.next_pair(p);
+        const int pos0 = unit.y * kDec8Stage;
+        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + kDec8Stage - 1 > hi0;
+        do_stage<TYPE, D, NT>(st, rw, qs, ring.base + s * G::kStageBytes, ks, vs, masked, pos0, lo0, hi0, p.n);
+        ++ring.used;
+        --left;
+        __syncwarp();  // every lane is done with the stage
     }
-    if (!ok && lane == 0) {
-        // Let every copy this warp started land before the CTA exits.
-        volatile int none = 0;
-        for (uint32_t k = ring.used; k < ring.issued; ++k)
-            mbar_wait(&ring.full[k % G::kStages], (k / G::kStages) & 1, &none, nullptr, p.timeout_ns);
+    if (!ok) {
+        run = -1;
+        if (lane == 0) {  // let every copy this warp started land before the CTA exits
+            volatile int none = 0;
+            for (uint32_t k = ring.used; k < ring.issued; ++k)
+                wait_long(&ring.full[k % G::kStages], (k / G::kStages) & 1, &none, nullptr, p.timeout_ns);
+        }
+        __syncwarp();
     }
-    __syncwarp();
+    // The warps' last runs, joined where neighbours share one.
+    if (lane == 0) last_run[warp] = run;
+    __syncthreads();
+    int lo = warp, hi = warp;
+    if (run >= 0) {
+        while (lo > 0 && last_run[lo - 1] == run) --lo;
+        while (hi + 1 < G::kWarps && last_run[hi + 1] == run) ++hi;
+        const long long row = row_at(p, gw, run >> 1, run & 1);
+        float* own = reinterpret_cast<float*>(__cvta_shared_to_generic(base));  // over the ring
+        store_state8<D, NT>(st, p.R, lo == hi ? part_ml(p) + row : reinterpret_cast<float2*>(own + 8 * NT * D),
+                            lo == hi ? part_o(p) + row * D : own);
+    }
+    __syncthreads();
+    if (lo < hi)
+        join_states<D, NT>(p, reinterpret_cast<const uint8_t*>(__cvta_shared_to_generic(base)) - (warp - lo) * G::kWarpBytes,
+                           hi - lo + 1, warp - lo, row_at(p, cta * G::kWarps + lo, run >> 1, run & 1));
 }
 
 // ---------------------------------------------------------------- combine
 
-// One CTA per query row, 1 to 8 warps: each warp joins every so-many-th of the row's
+// One CTA per query row, 1 to 4 warps: each warp joins every so-many-th of the row's
 // partial states, a lane holding D / 32 columns, and the warps' sums meet in shared
 // memory in warp order.
-constexpr int kCombineWarps = 8;
+constexpr int kCombineWarps = 4;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(const __grid_constant__ Decode8Params p, int most)
+__global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(const __grid_constant__ Decode8Params p, int grid)
 {
     constexpr int C = D / 32;  // columns per lane
-    __shared__ float red_m[2][kCombineWarps], red_l[2][kCombineWarps], red_o[2][kCombineWarps][D];
-    __shared__ Plan s_plan;
-    __shared__ int s_before, s_T;
+    constexpr int kWarps = D8<D, NT>::kWarps;
+    __shared__ float red_m[2][kCombineWarps], red_l[2][kCombineWarps];
+    __shared__ alignas(16) float red_o[2][kCombineWarps][D];
+    __shared__ uint32_t s_word;
+    __shared__ int s_before[kCombineWarps], s_T[kCombineWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = (int)blockDim.x >> 5;
     const int pair = (int)(blockIdx.x / (unsigned)p.R), r = (int)(blockIdx.x % (unsigned)p.R);
     const int b = pair / p.Hkv, hk = pair % p.Hkv, tok = r % p.n;
     const float gate = p.gate[(long long)b * p.n + tok];
     const bool sel = takes_global(gate, *p.tau);
-    if (warp == 0) {
-        int T = 0, before = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const Plan pl = b0 + lane < p.B ? plan_of(p, b0 + lane) : Plan{0, 0, 0, 0};
-            const int un = pl.units();
-            T += (int)__reduce_add_sync(0xffffffffu, un) * p.Hkv;
-            before += (int)__reduce_add_sync(0xffffffffu, b0 + lane < b ? un : 0) * p.Hkv;
-            if (b0 + lane == b) s_plan = pl;
-        }
-        if (lane == 0) s_T = T, s_before = before;
+    int T = 0, before = 0;
+    for (int i = tid; i < p.B; i += (int)blockDim.x) {
+        const uint32_t w = word_from(p, i);
+        const int un = Plan(p, w).units() * p.Hkv;
+        T += un;
+        if (i < b) before += un;
+        if (i == b) s_word = w;
     }
+    T = (int)__reduce_add_sync(0xffffffffu, T);
+    before = (int)__reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) s_T[warp] = T, s_before[warp] = before;
     __syncthreads();
-    const Plan pl = s_plan;
+    T = before = 0;
+    for (int w = 0; w < nw; ++w) T += s_T[w], before += s_before[w];
+    const Plan pl(p, s_word);
     if (p.selected && hk == 0 && r < p.n && tid == 0) p.selected[(long long)b * p.n + r] = sel ? 1 : 0;
     uint16_t* out = p.out + ((long long)pair * p.R + r) * D;
     if (pl.len < p.n - tok) {  // the token lies before the sequence's start (or the length is invalid)
         for (int c = tid; c < D; c += (int)blockDim.x) out[c] = 0;
         return;
     }
-    const Shares sh(s_T, most, least_units(NT));
-    const int u0 = s_before + hk * pl.units();
-    // slots of the states inside the window (kind 0) and, for a global token, before it (kind 1)
-    const int w_in = sh.warp_of(u0 + pl.out), n_in = sh.warp_of(u0 + pl.units() - 1) - w_in + 1;
-    const int w_out = sh.warp_of(u0), n_out = sel && pl.out ? sh.warp_of(u0 + pl.out - 1) - w_out + 1 : 0;
-    const long long at[2] = {row_at(p, w_in, pair, 0) + r, row_at(p, w_out, pair, 1) + r};
-    const int cnt[2] = {n_in, n_out};
+    // Where the row's states lie: for each CTA that the run reaches into, the slot of the run's
+    // first warp there; and the run's last warp's own where its share goes on behind the run.
+    const Shares ctas(T, grid);
+    const int u0 = before + hk * pl.units();
+    const int from[2] = {u0 + pl.out, u0}, to[2] = {u0 + pl.units(), u0 + (sel ? pl.out : 0)};
+    int cnt[2], extra[2];
+    long long row0[2], row1[2], row_x[2];
+    #pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        cnt[k] = extra[k] = 0;
+        row0[k] = row1[k] = row_x[k] = 0;
+        if (from[k] >= to[k]) continue;
+        const int c0 = ctas.of(from[k]), c1 = ctas.of(to[k] - 1);
+        const Shares s0(ctas.first(c0 + 1) - ctas.first(c0), kWarps);
+        const Shares s1(ctas.first(c1 + 1) - ctas.first(c1), kWarps);
+        const int v0 = s0.of(from[k] - ctas.first(c0)), v1 = s1.of(to[k] - 1 - ctas.first(c1));
+        cnt[k] = c1 - c0 + 1;
+        row0[k] = row_at(p, c0 * kWarps + v0, pair, k) + r;      // in the first CTA
+        row1[k] = row_at(p, (c0 + 1) * kWarps, pair, k) + r;     // in the next, kWarps slots from one to the next
+        extra[k] = s1.first(v1 + 1) != to[k] - ctas.first(c1) && v1 != (c1 == c0 ? v0 : 0);
+        row_x[k] = row_at(p, c1 * kWarps + v1, pair, k) + r;
+    }
     const float2* ml = part_ml(p);
     const float* po = part_o(p) + lane * C;
-    const long long step = 2LL * p.R;
+    const long long step = 2LL * p.R * kWarps;
+    auto row_of = [&](int k, int i) {
+        return i == 0 ? row0[k] : i < cnt[k] ? row1[k] + (i - 1) * step : row_x[k];
+    };
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Each warp joins its states four at a time, all of their loads in flight together; then
+    // warp 0 joins the warps'.
     float m[2], l[2], o[2][C];
     #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        float mx = -INFINITY;
-        for (int i = tid; i < cnt[k]; i += (int)blockDim.x) mx = fmaxf(mx, ml[at[k] + i * step].x);
-        #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        if (lane == 0) red_m[k][warp] = mx;
-    }
-    __syncthreads();
-    #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        m[k] = -INFINITY;
-        for (int w = 0; w < nw; ++w) m[k] = fmaxf(m[k], red_m[k][w]);
-        l[k] = 0.f;
+        m[k] = -INFINITY, l[k] = 0.f;
         #pragma unroll
         for (int c = 0; c < C; ++c) o[k][c] = 0.f;
-        #pragma unroll 4
-        for (int i = warp; i < cnt[k]; i += nw) {
-            const long long row = at[k] + i * step;
-            const float2 s = ml[row];
-            float v[C];
-            if (C == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(po + row * D);
-                v[0] = x.x, v[1] = x.y, v[C - 2] = x.z, v[C - 1] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(po + row * D);
-                v[0] = x.x, v[1] = x.y;
-            }
-            const float f = s.x == -INFINITY ? 0.f : exp2f(s.x - m[k]);
-            l[k] = fmaf(f, s.y, l[k]);
+    }
+    auto load = [&](const float* at, float (&v)[C]) {
+        if (C == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(at);
+            v[0] = x.x, v[1] = x.y, v[C - 2] = x.z, v[C - 1] = x.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(at);
+            v[0] = x.x, v[1] = x.y;
+        }
+    };
+    auto join = [&](int k, float mi, float li, const float (&v)[C]) {
+        const float mn = fmaxf(m[k], mi);
+        const float f0 = m[k] == -INFINITY ? 0.f : exp2f(m[k] - mn), f1 = mi == -INFINITY ? 0.f : exp2f(mi - mn);
+        m[k] = mn;
+        l[k] = fmaf(f0, l[k], f1 * li);
+        #pragma unroll
+        for (int c = 0; c < C; ++c) o[k][c] = fmaf(f0, o[k][c], f1 * v[c]);
+    };
+    const int all = cnt[0] + extra[0] + cnt[1] + extra[1];
+    #pragma unroll 1
+    for (int i0 = warp; i0 < all; i0 += 4 * nw) {
+        float2 s[4];
+        float v[4][C];
+        int kind[4];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * nw;
+            kind[j] = i >= cnt[0] + extra[0];
+            s[j] = make_float2(-INFINITY, 0.f);
             #pragma unroll
-            for (int c = 0; c < C; ++c) o[k][c] = fmaf(f, v[c], o[k][c]);
+            for (int c = 0; c < C; ++c) v[j][c] = 0.f;
+            if (i < all) {
+                const long long row = kind[j] ? row_of(1, i - cnt[0] - extra[0]) : row_of(0, i);
+                s[j] = ml[row];
+                load(po + row * D, v[j]);
+            }
+        }
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (kind[j]) join(1, s[j].x, s[j].y, v[j]);
+            else join(0, s[j].x, s[j].y, v[j]);
         }
     }
     if (nw > 1) {
         #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (lane == 0) red_l[k][warp] = l[k];
+            if (lane == 0) red_m[k][warp] = m[k], red_l[k][warp] = l[k];
             #pragma unroll
             for (int c = 0; c < C; ++c) red_o[k][warp][lane * C + c] = o[k][c];
         }
         __syncthreads();
         if (warp > 0) return;
-        #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            for (int w = 1; w < nw; ++w) {
-                l[k] += red_l[k][w];
-                #pragma unroll
-                for (int c = 0; c < C; ++c) o[k][c] += red_o[k][w][lane * C + c];
+        #pragma unroll 1
+        for (int w = 1; w < nw; ++w)
+            #pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float v[C];
+                load(&red_o[k][w][lane * C], v);
+                join(k, red_m[k][w], red_l[k][w], v);
             }
     }
     float val[C];
@@ -839,8 +1016,8 @@ cudaError_t launch_tdn(const Decode8Params& p, cudaStream_t stream)
     decode8_partial_kernel<TYPE, D, NT><<<grid, D8<D, NT>::kThreads, D8<D, NT>::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // Warps per row: about four states for each, by the most that a row can have.
-    const long long states = ((long long)grid * D8<D, NT>::kWarps) / ((long long)p.B * p.Hkv) + 2;
-    const int warps = states <= 4 ? 1 : states <= 8 ? 2 : states <= 16 ? 4 : kCombineWarps;
+    const long long states = grid / ((long long)p.B * p.Hkv) + 2;
+    const int warps = states <= 4 ? 1 : states <= 8 ? 2 : kCombineWarps;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.R));
     cfg.blockDim = dim3(32 * warps);
@@ -850,7 +1027,7 @@ cudaError_t launch_tdn(const Decode8Params& p, cudaStream_t stream)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode8_combine_kernel<D, NT>, p, grid * D8<D, NT>::kWarps);
+    return cudaLaunchKernelEx(&cfg, decode8_combine_kernel<D, NT>, p, grid);
 }
 
 template <int TYPE, int D>
@@ -874,3 +1051,4 @@ cudaError_t launch_decode8(const Decode8Params& p, int type, int d, cudaStream_t
 }
 
 }  // namespace logo
+

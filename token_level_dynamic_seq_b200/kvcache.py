@@ -33,7 +33,7 @@ class Cache8:
     The tensors are the caller's; :func:`cache8` allocates a set."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "k_tail", "v_tail", "B", "Hkv", "Lmax", "d", "block", "device",
-                 "_desc", "_ref")
+                 "index", "_desc", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale, k_tail, v_tail):
         if k.dim() != 4 or k_tail.dim() != 5:
@@ -60,6 +60,7 @@ class Cache8:
                 raise ValueError("the cache's tensors lie on different devices")
         self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail = tensors
         self.B, self.Hkv, self.Lmax, self.d, self.block, self.device = B, H, L, d, block, k.device
+        self.index = k.get_device() if k.is_cuda else -1
         self._desc = _logo.Cache8Desc(B, H, L, d, block, _TYPES[k.dtype], *(t.data_ptr() for t in tensors))
         self._ref = ctypes.byref(self._desc)
 
@@ -76,27 +77,31 @@ def cache8(B: int, Hkv: int, Lmax: int, d: int, device, dtype=torch.float8_e4m3f
                   new(tail, torch.bfloat16), new(tail, torch.bfloat16))
 
 
-def _on(cache: Cache8, **tensors):
-    """Every tensor on the cache's device, which is the current one, contiguous and of its type."""
-    dev = cache.device
-    if dev.type != "cuda":
+def _lib_on(cache: Cache8):
+    """The library, for a cache on the current device."""
+    if cache.index < 0:
         raise ValueError("expected a cache of CUDA tensors")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache lies on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, (t, dtype) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"{name} lies on {t.device}, the cache on {dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous tensor")
+    if cache.index != torch.cuda.current_device():
+        raise ValueError(f"the cache lies on {cache.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _logo._lib or _logo.load_library()
 
 
-def _count(t, n: int, name: str):
-    if t is not None and t.numel() < n:
-        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+def _at(cache: Cache8, t, dtype, count: int, name: str):
+    """Address of a tensor that a call takes: of its type, contiguous, on the cache's device, with `count` elements."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} lies on {t.device}, the cache on {cache.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.numel() < count:
+        raise ValueError(f"{name}: expected {count} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _queue(cache: Cache8, stream):
+    """The stream's handle; the current stream's without making an object of it."""
+    return torch._C._cuda_getCurrentRawStream(cache.index) if stream is None else stream.cuda_stream
 
 
 def _used_on(stream, *tensors):
@@ -113,10 +118,6 @@ def _new_ws(cache: Cache8, size: int, stream):
     return ws
 
 
-def _status_ws(cache: Cache8, ws, stream):
-    return _new_ws(cache, 256, stream) if ws is None else ws
-
-
 def _rows_shape(cache: Cache8, rows: int, cu_seqlens, max_seqlen):
     if cu_seqlens is None:
         return _logo.Shape(cache.B, cache.Hkv, cache.Hkv, rows, cache.d, None, cache.B, rows)
@@ -124,7 +125,8 @@ def _rows_shape(cache: Cache8, rows: int, cu_seqlens, max_seqlen):
         raise ValueError("max_seqlen is required with cu_seqlens (the library never reads device data on the host)")
     if cu_seqlens.numel() != cache.B + 1:
         raise ValueError(f"cu_seqlens: expected {cache.B + 1} offsets, got {cu_seqlens.numel()}")
-    return _logo.Shape(1, cache.Hkv, cache.Hkv, rows, cache.d, cu_seqlens.data_ptr(), cache.B, int(max_seqlen))
+    cu = _at(cache, cu_seqlens, torch.int32, 0, "cu_seqlens")
+    return _logo.Shape(1, cache.Hkv, cache.Hkv, rows, cache.d, cu, cache.B, int(max_seqlen))
 
 
 def cache8_append(cache: Cache8, k, v, start, ws=None, cu_seqlens=None, max_seqlen=None, new_len=None, stream=None):
@@ -134,18 +136,19 @@ def cache8_append(cache: Cache8, k, v, start, ws=None, cu_seqlens=None, max_seql
     ``max_seqlen``.  ``start[b]`` may be the sequence's length so far, an earlier multiple of the block, or a
     position in the sequence's latest append (its last two blocks): rejected drafts are appended over.
     ``new_len`` (int32 [B]) receives start + n."""
-    _on(cache, k=(k, torch.bfloat16), v=(v, torch.bfloat16), start=(start, torch.int32),
-        cu_seqlens=(cu_seqlens, torch.int32), new_len=(new_len, torch.int32), ws=(ws, torch.uint8))
-    want = (cache.B if cu_seqlens is None else 1, cache.Hkv, k.shape[2] if k.dim() == 4 else -1, cache.d)
+    lib = _lib_on(cache)
+    B, H, d = cache.B, cache.Hkv, cache.d
+    n = k.shape[2] if k.dim() == 4 else -1
+    want = (B if cu_seqlens is None else 1, H, n, d)
     if tuple(k.shape) != want or v.shape != k.shape:
         raise ValueError(f"k, v: expected {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    _count(start, cache.B, "start")
-    _count(new_len, cache.B, "new_len")
-    shape = _rows_shape(cache, k.shape[2], cu_seqlens, max_seqlen)
-    ws = _status_ws(cache, ws, stream)
-    _logo._raise(_logo.load_library().logo_cache8_append(
-        cache._ref, k.data_ptr(), v.data_ptr(), ctypes.byref(shape), start.data_ptr(),
-        None if new_len is None else new_len.data_ptr(), ws.data_ptr(), ws.numel(), _logo._stream(stream)))
+    ws = _new_ws(cache, 256, stream) if ws is None else ws
+    shape = _rows_shape(cache, n, cu_seqlens, max_seqlen)
+    _logo._raise(lib.logo_cache8_append(
+        cache._ref, _at(cache, k, torch.bfloat16, 0, "k"), _at(cache, v, torch.bfloat16, 0, "v"), shape,
+        _at(cache, start, torch.int32, B, "start"),
+        None if new_len is None else _at(cache, new_len, torch.int32, B, "new_len"),
+        _at(cache, ws, torch.uint8, 0, "ws"), ws.numel(), _queue(cache, stream)))
 
 
 def cache8_read(cache: Cache8, start, rows: int, ws=None, cu_seqlens=None, max_seqlen=None, out=None, stream=None):
@@ -153,22 +156,22 @@ def cache8_read(cache: Cache8, start, rows: int, ws=None, cu_seqlens=None, max_s
 
     With ``cu_seqlens`` int32 [B + 1] and ``max_seqlen`` the rows of all sequences come packed,
     [1, Hkv, rows, d] (``rows`` is their total).  ``out`` = (k, v) to write into."""
+    lib = _lib_on(cache)
     rows = int(rows)
     want = (cache.B if cu_seqlens is None else 1, cache.Hkv, rows, cache.d)
     if out is None:
-        out = tuple(torch.empty(want, dtype=torch.bfloat16, device=cache.device) for _ in range(2))
+        out = (torch.empty(want, dtype=torch.bfloat16, device=cache.device),
+               torch.empty(want, dtype=torch.bfloat16, device=cache.device))
         _used_on(stream, *out)
     k, v = out
-    _on(cache, k_out=(k, torch.bfloat16), v_out=(v, torch.bfloat16), start=(start, torch.int32),
-        cu_seqlens=(cu_seqlens, torch.int32), ws=(ws, torch.uint8))
     if tuple(k.shape) != want or tuple(v.shape) != want:
         raise ValueError(f"out: expected {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    _count(start, cache.B, "start")
+    ws = _new_ws(cache, 256, stream) if ws is None else ws
     shape = _rows_shape(cache, rows, cu_seqlens, max_seqlen)
-    ws = _status_ws(cache, ws, stream)
-    _logo._raise(_logo.load_library().logo_cache8_read(
-        cache._ref, start.data_ptr(), ctypes.byref(shape), k.data_ptr(), v.data_ptr(), ws.data_ptr(), ws.numel(),
-        _logo._stream(stream)))
+    _logo._raise(lib.logo_cache8_read(
+        cache._ref, _at(cache, start, torch.int32, cache.B, "start"), shape, _at(cache, k, torch.bfloat16, 0, "k_out"),
+        _at(cache, v, torch.bfloat16, 0, "v_out"), _at(cache, ws, torch.uint8, 0, "ws"), ws.numel(),
+        _queue(cache, stream)))
     return k, v
 
 
@@ -186,24 +189,22 @@ def decode8(q, cache: Cache8, cache_len, gate, tau, window: int, ws=None, scale:
     (the new tokens included), ``gate`` fp32 [B, n], ``tau`` fp32 [1].  Returns (out, like q; selected int32 [B, n])."""
     if q.dim() not in (3, 4) or q.shape[0] != cache.B or q.shape[-1] != cache.d:
         raise ValueError(f"q: expected [{cache.B}, Hq, n, {cache.d}], got {tuple(q.shape)}")
+    lib = _lib_on(cache)
+    B, Hq = cache.B, q.shape[1]
     n = q.shape[2] if q.dim() == 4 else 1
-    _on(cache, q=(q, torch.bfloat16), cache_len=(cache_len, torch.int32), gate=(gate, torch.float32),
-        tau=(tau, torch.float32), ws=(ws, torch.uint8), out=(out, torch.bfloat16), selected=(selected, torch.int32))
     if ws is None:
-        ws = decode8_workspace(cache, q.shape[1], n, stream)
+        ws = decode8_workspace(cache, Hq, n, stream)
     if out is None:
         out = torch.empty_like(q)
         _used_on(stream, out)
     elif out.shape != q.shape:
         raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
     if selected is None:
-        selected = torch.empty((cache.B, n), dtype=torch.int32, device=cache.device)
+        selected = torch.empty((B, n), dtype=torch.int32, device=cache.device)
         _used_on(stream, selected)
-    _count(cache_len, cache.B, "cache_len")
-    _count(gate, cache.B * n, "gate")
-    _count(tau, 1, "tau")
-    _count(selected, cache.B * n, "selected")
-    _logo._raise(_logo.load_library().logo_decode8(
-        q.data_ptr(), cache._ref, cache_len.data_ptr(), gate.data_ptr(), tau.data_ptr(), q.shape[1], n, int(window),
-        float(scale), out.data_ptr(), selected.data_ptr(), ws.data_ptr(), ws.numel(), _logo._stream(stream)))
+    _logo._raise(lib.logo_decode8(
+        _at(cache, q, torch.bfloat16, 0, "q"), cache._ref, _at(cache, cache_len, torch.int32, B, "cache_len"),
+        _at(cache, gate, torch.float32, B * n, "gate"), _at(cache, tau, torch.float32, 1, "tau"), Hq, n, int(window),
+        float(scale), _at(cache, out, torch.bfloat16, 0, "out"), _at(cache, selected, torch.int32, B * n, "selected"),
+        _at(cache, ws, torch.uint8, 0, "ws"), ws.numel(), _queue(cache, stream)))
     return out, selected
