@@ -70,10 +70,9 @@ namespace {
 #ifndef LOGO_DEC8_RING
 #define LOGO_DEC8_RING 16384
 #endif
-#ifndef LOGO_DEC8_KUNROLL
-#define LOGO_DEC8_KUNROLL 2
+#ifndef LOGO_DEC8_UG
+#define LOGO_DEC8_UG 2
 #endif
-constexpr int kKUnroll = LOGO_DEC8_KUNROLL;  // of the loop over head-dimension pairs of the scores
 constexpr float kPBias = 15.f;  // P is held times 2^15: the state's m is the maximum less 15
 constexpr int kWordsMax = 1024; // sequences whose length and gate decision a CTA keeps in shared memory
 
@@ -196,18 +195,20 @@ __device__ __forceinline__ float* part_o(const Decode8Params& p)
 
 // ---------------------------------------------------------------- fragments
 
+template <int OFF>
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
 {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+                 : "r"(addr), "n"(OFF));
 }
 
+template <int OFF>
 __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4])
 {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+                 : "r"(addr), "n"(OFF));
 }
 
 __device__ __forceinline__ uint32_t movm(uint32_t x)
@@ -226,6 +227,17 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from C = (c0, c1, c2, c3) (a zero costs no register).
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1, float c0, float c1, float c2, float c3)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
@@ -299,7 +311,8 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
 // t), a share of their sums, and of O^T the rows 16 u + 2g + h at o[u][nt][2h + c].
 template <int D, int NT>
 struct State8 {
-    float m[NT][2], l[NT][2];
+    float m[NT][2];
+    float l[NT][2];
     float o[D / 16][NT][4];
     __device__ __forceinline__ void init()
     {
@@ -308,9 +321,7 @@ struct State8 {
         #pragma unroll
         for (int u = 0; u < D / 16; ++u)
             #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                #pragma unroll
-                for (int e = 0; e < 4; ++e) o[u][nt][e] = 0.f;
+            for (int nt = 0; nt < NT; ++nt) o[u][nt][0] = o[u][nt][1] = o[u][nt][2] = o[u][nt][3] = 0.f;
     }
 };
 
@@ -342,7 +353,8 @@ __device__ __forceinline__ void store_state8(State8<D, NT>& st, int R, float2* m
             store_if(r < R && g == 0, ml + r, st.m[nt][c], st.l[nt][c]);
             float* row = o + r * D + 2 * g;
             #pragma unroll
-            for (int u = 0; u < D / 16; ++u) store_if(r < R, row + 16 * u, st.o[u][nt][c], st.o[u][nt][2 + c]);
+            for (int u = 0; u < D / 16; ++u)
+                store_if(r < R, row + 16 * u, st.o[u][nt][c], st.o[u][nt][2 + c]);
         }
 }
 
@@ -541,20 +553,16 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
 {
     using G = D8<D, NT>;
     constexpr int MT = G::MT;
+    static_assert(MT == 2, "a stage is one ldmatrix of V^T per 16 columns");
     const int lane = threadIdx.x & 31, g = lane >> 2;
-    const int kr = (lane & 7) + 8 * ((lane >> 3) & 1), ku = lane >> 4;  // ldmatrix roles: row, 16-byte unit
     const uint32_t tileV = tileK + G::kTile;
     if (masked && mask_values<TYPE, D>(tileV, pos0, lo0, hi0, n) && TYPE == kCacheE4M3)
         place_nan<D, NT>(tileV, pos0, lo0, hi0, n, rw, st);
-    // S^T = K q^T: rows = positions 16 mt + g (+ 8), columns = query rows
+    // S^T = K q^T: rows = positions 16 mt + g (+ 8), columns = query rows.  ldmatrix: lane's row
+    // lane mod 16 of the 16, 16-byte unit 2 kk + lane / 16; the swizzle turns into an exclusive or.
     float sc[MT][NT][4];
+    const uint32_t kat = swz<D>(tileK, lane & 15, lane >> 4);
     #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            #pragma unroll
-            for (int x = 0; x < 4; ++x) sc[mt][nt][x] = rw.s0[nt][x & 1];
-    #pragma unroll kKUnroll
     for (int kk = 0; kk < D / 32; ++kk) {
         uint2 b0[NT], b1[NT];
         #pragma unroll
@@ -562,31 +570,43 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
             b0[nt] = qs[((2 * kk) * NT + nt) * 32 + lane];
             b1[nt] = qs[((2 * kk + 1) * NT + nt) * 32 + lane];
         }
+        // every product of a step before the first that continues one
+        uint32_t x[MT][4], y[MT][4];
         #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            uint32_t w[4], x[4], y[4];
-            ldsm4(swz<D>(tileK, 16 * mt + kr, 2 * kk + ku), w);
+            uint32_t w[4];
+            if (mt == 0)
+                ldsm4<0>(kat ^ (kk << 5), w);
+            else
+                ldsm4<16 * D>(kat ^ (kk << 5), w);
             #pragma unroll
-            for (int q = 0; q < 4; ++q) to_f16<TYPE>(w[q], x[q], y[q]);
+            for (int q = 0; q < 4; ++q) to_f16<TYPE>(w[q], x[mt][q], y[mt][q]);
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                mma_f16(sc[mt][nt], x[0], x[1], y[0], y[1], b0[nt].x, b0[nt].y);
-                mma_f16(sc[mt][nt], x[2], x[3], y[2], y[3], b1[nt].x, b1[nt].y);
+                if (kk == 0)
+                    mma_f16_from(sc[mt][nt], x[mt][0], x[mt][1], y[mt][0], y[mt][1], b0[nt].x, b0[nt].y, rw.s0[nt][0],
+                                 rw.s0[nt][1], rw.s0[nt][0], rw.s0[nt][1]);
+                else
+                    mma_f16(sc[mt][nt], x[mt][0], x[mt][1], y[mt][0], y[mt][1], b0[nt].x, b0[nt].y);
             }
         }
+        #pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(sc[mt][nt], x[mt][2], x[mt][3], y[mt][2], y[mt][3], b1[nt].x, b1[nt].y);
     }
-    // online softmax
+    // Online softmax.  The maximum is taken over the products before their (positive) factor,
+    // which meets them in the exponent's multiply-add.
     uint32_t pb[MT][NT][2];
     float al[NT][2];
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+        float f[2], nr[2];
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const float f = ks * rw.qf[nt][c];
-            #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                #pragma unroll
-                for (int h = 0; h < 2; ++h) sc[mt][nt][2 * h + c] *= f;
+            f[c] = ks * rw.qf[nt][c];
+            f[c] = f[c] < 1.17549435e-38f ? 1.17549435e-38f : f[c];  // so that it leaves -inf as it is
             if (masked) {
                 const int lo = lo0 + rw.tok[nt][c] - pos0 - g, hi = hi0 + rw.tok[nt][c] - pos0 - g;
                 #pragma unroll
@@ -595,32 +615,30 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
                     for (int h = 0; h < 2; ++h)
                         if (16 * mt + 8 * h < lo || 16 * mt + 8 * h > hi) sc[mt][nt][2 * h + c] = -INFINITY;
             }
-            float mx = -INFINITY;
-            #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mx = fmax3(mx, sc[mt][nt][c], sc[mt][nt][2 + c]);
+            float mx = fmax3(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), sc[1][nt][c], sc[1][nt][2 + c]);
             #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(st.m[nt][c], mx - kPBias);
-            const float r = mn == -INFINITY ? 0.f : mn;
-            al[nt][c] = fast_exp2(st.m[nt][c] - r);  // 0 while nothing was seen
+            const float mn = fmaxf(st.m[nt][c], fmaf(mx, f[c], -kPBias));
+            nr[c] = mn == -INFINITY ? 0.f : -mn;
+            al[nt][c] = fast_exp2(st.m[nt][c] + nr[c]);  // 0 while nothing was seen
             st.m[nt][c] = mn;
-            float sum = 0.f;
-            #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float x = fast_exp2(sc[mt][nt][2 * h + c] - r);
-                    sc[mt][nt][2 * h + c] = x;
-                    sum += x;
-                }
-            st.l[nt][c] = fmaf(st.l[nt][c], al[nt][c], sum);
         }
-        // P^T fragments: the score fragment's 8x8 quarters transposed in registers
+        float sum[2] = {0.f, 0.f};
         #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                pb[mt][nt][h] = movm(pack_f16x2(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]));
+            for (int h = 0; h < 2; ++h) {
+                float x[2];
+                #pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    x[c] = fast_exp2(fmaf(sc[mt][nt][2 * h + c], f[c], nr[c]));
+                    sum[c] += x[c];
+                }
+                // P^T fragment: the score fragment's 8x8 quarter transposed in registers
+                pb[mt][nt][h] = movm(pack_f16x2(x[0], x[1]));
+            }
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) st.l[nt][c] = fmaf(st.l[nt][c], al[nt][c], sum[c]);
     }
     // O^T = O^T alpha + (V^T P^T) vs; most stages leave every maximum as it is
     bool moved = false;
@@ -628,51 +646,53 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
     for (int nt = 0; nt < NT; ++nt) moved |= al[nt][0] != 1.f || al[nt][1] != 1.f;
     if (__any_sync(0xffffffffu, moved)) {
         #pragma unroll
-        for (int u = 0; u < D / 16; ++u)
+        for (int nt = 0; nt < NT; ++nt)
             #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < D / 16; ++u)
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) st.o[u][nt][e] *= al[nt][e & 1];
     }
-    float o0[NT][4];  // what the products start at: zero, or (int8) -128 2^-24 sum P
+    float o0[NT][2];  // what the products start at: zero, or (int8) -128 2^-24 sum P
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) o0[nt][e] = 0.f;
+        o0[nt][0] = o0[nt][1] = 0.f;
         if (TYPE == kCacheInt8) {
-            #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                mma_f16(o0[nt], kOnes, kOnes, kOnes, kOnes, pb[mt][nt][0], pb[mt][nt][1]);
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) o0[nt][e] *= kInt8Shift;
+            float ones[4];
+            mma_f16_from(ones, kOnes, kOnes, kOnes, kOnes, pb[0][nt][0], pb[0][nt][1], 0.f, 0.f, 0.f, 0.f);
+            mma_f16(ones, kOnes, kOnes, kOnes, kOnes, pb[1][nt][0], pb[1][nt][1]);
+            o0[nt][0] = ones[0] * kInt8Shift;
+            o0[nt][1] = ones[1] * kInt8Shift;
         }
     }
     if (TYPE == kCacheInt8) vs *= kInt8Unit;
+    const uint32_t vat = swz<D>(tileV, lane, 0);
+    constexpr int UG = LOGO_DEC8_UG;  // column groups of 16 in flight
     #pragma unroll
-    for (int u = 0; u < D / 16; ++u) {
-        float acc[NT][4];
+    for (int u0 = 0; u0 < D / 16; u0 += UG) {
+        uint32_t ev[UG][4], od[UG][4];
+        float acc[UG][NT][4];
         #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < UG; ++j) {
+            uint32_t w[4];
+            ldsm4t<0>(vat ^ ((u0 + j) << 4), w);
             #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][e] = o0[nt][e];
-        #pragma unroll
-        for (int h = 0; h < MT / 2; ++h) {
-            uint32_t w[4], ev[4], od[4];
-            ldsm4t(swz<D>(tileV, 32 * h + lane, u), w);
+            for (int i = 0; i < 4; ++i) to_f16_pairs<TYPE>(w[i], ev[j][i], od[j][i]);
             #pragma unroll
-            for (int i = 0; i < 4; ++i) to_f16_pairs<TYPE>(w[i], ev[i], od[i]);
-            #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(acc[nt], ev[2 * k], od[2 * k], ev[2 * k + 1], od[2 * k + 1], pb[2 * h + k][nt][0],
-                            pb[2 * h + k][nt][1]);
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16_from(acc[j][nt], ev[j][0], od[j][0], ev[j][1], od[j][1], pb[0][nt][0], pb[0][nt][1], o0[nt][0],
+                             o0[nt][1], o0[nt][0], o0[nt][1]);
         }
         #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < UG; ++j)
             #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                st.o[u][nt][e] = fmaf(acc[nt][e], vs, st.o[u][nt][e]);
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(acc[j][nt], ev[j][2], od[j][2], ev[j][3], od[j][3], pb[1][nt][0], pb[1][nt][1]);
+        #pragma unroll
+        for (int j = 0; j < UG; ++j)
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) st.o[u0 + j][nt][e] = fmaf(acc[j][nt][e], vs, st.o[u0 + j][nt][e]);
     }
 }
 
