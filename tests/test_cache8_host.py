@@ -169,10 +169,16 @@ def grids():
     return {448: e4m3, 127: [Fraction(i) for i in range(128)]}
 
 
+def snap(y):
+    """y to 19 significant bits, as the kernel does it in fp32: u = 33 y, then u - (u - y)."""
+    u = (y * np.float32(33)).astype(np.float32)
+    return (u - (u - y).astype(np.float32)).astype(np.float32)
+
+
 @pytest.mark.parametrize("top", [448, 127])
-def test_reciprocal_and_19_bits_round_as_the_exact_quotient(top):
-    """fl(x * fl(Q / a)) rounded to 19 significant bits lies on the same side of every rounding border as the
-    exact x Q / a, borders included, for all 8-bit significands of x and a."""
+def test_snapped_product_rounds_as_the_exact_quotient(top):
+    """y = fl(x * fl(Q / a)), rounded to 19 significant bits, lies on the same side of every rounding border as the exact x Q / a,
+    borders included, for all 8-bit significands of x and a."""
     values = grids()[top]
     borders = [(a + b) / 2 for a, b in zip(values, values[1:])]
     fine = np.array([float(b) for b in borders])           # borders are exact in fp64
@@ -183,7 +189,7 @@ def test_reciprocal_and_19_bits_round_as_the_exact_quotient(top):
         keep = x <= a
         inv = (np.float32(top) / a).astype(np.float32)
         y = (x * inv).astype(np.float32)
-        snapped = ((y.view(np.uint32) + np.uint32(0x10)) & np.uint32(0xffffffe0)).view(np.float32).astype(np.float64)
+        snapped = snap(y).astype(np.float64)
         # exact comparison with the nearest border, in whole numbers
         idx = np.searchsorted(fine, snapped)
         for d in (-1, 0):
@@ -202,8 +208,7 @@ def test_reciprocal_and_19_bits_round_as_the_exact_quotient(top):
             continue
         inv = np.float32(top) / np.float32(A)
         y = np.float32(np.float32(X * 2.0 ** -s) * inv)
-        y = np.array([y], np.float32).view(np.uint32)
-        y = float(((y + np.uint32(0x10)) & np.uint32(0xffffffe0)).view(np.float32)[0])
+        y = float(snap(np.array([y], np.float32))[0])
         assert nearest(Fraction(y), borders, values) == nearest(Fraction(X * top, A << s), borders, values)
 
 

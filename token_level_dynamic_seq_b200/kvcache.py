@@ -88,15 +88,15 @@ def _lib_on(cache: Cache8):
 
 def _at(cache: Cache8, t, dtype, count: int, name: str):
     """Address of a tensor that a call takes: of its type, contiguous, on the cache's device, with `count` elements."""
+    if t.dtype is dtype and t.get_device() == cache.index and t.is_contiguous() and t.numel() >= count:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.get_device() != cache.index:
         raise ValueError(f"{name} lies on {t.device}, the cache on {cache.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    if t.numel() < count:
-        raise ValueError(f"{name}: expected {count} elements, got {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected {count} elements, got {t.numel()}")
 
 
 def _queue(cache: Cache8, stream):
@@ -160,8 +160,7 @@ def cache8_read(cache: Cache8, start, rows: int, ws=None, cu_seqlens=None, max_s
     rows = int(rows)
     want = (cache.B if cu_seqlens is None else 1, cache.Hkv, rows, cache.d)
     if out is None:
-        out = (torch.empty(want, dtype=torch.bfloat16, device=cache.device),
-               torch.empty(want, dtype=torch.bfloat16, device=cache.device))
+        out = cache.k_tail.new_empty(want), cache.k_tail.new_empty(want)
         _used_on(stream, *out)
     k, v = out
     if tuple(k.shape) != want or tuple(v.shape) != want:
@@ -200,7 +199,7 @@ def decode8(q, cache: Cache8, cache_len, gate, tau, window: int, ws=None, scale:
     elif out.shape != q.shape:
         raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
     if selected is None:
-        selected = torch.empty((B, n), dtype=torch.int32, device=cache.device)
+        selected = cache_len.new_empty((B, n))
         _used_on(stream, selected)
     _logo._raise(lib.logo_decode8(
         _at(cache, q, torch.bfloat16, 0, "q"), cache._ref, _at(cache, cache_len, torch.int32, B, "cache_len"),
