@@ -162,8 +162,8 @@ struct Shares {
     __device__ __forceinline__ Shares(int T, int most)
     {
         N = T < most ? T : most;
-        each = N ? (int)((unsigned)T / (unsigned)N) : 0;
-        rest = T - each * N;
+        each = T < most ? 1 : (int)((unsigned)T / (unsigned)most);  // T below `most`: shares of one unit
+        rest = T < most ? 0 : T - each * N;
     }
     __device__ __forceinline__ int first(int w) const { return w * each + (w < rest ? w : rest); }
     __device__ __forceinline__ int of(int u) const  // the share that unit u belongs to
@@ -410,7 +410,8 @@ __device__ __forceinline__ void issue_unit(const Decode8Params& p, const uint32_
     const uint32_t s = ring.issued % G::kStages;
     if ((threadIdx.x & 31) == 0) {
         uint8_t* dst = reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(ring.base + s * G::kStageBytes));
-        fence_proxy_async_smem();  // the warp's reads of this stage come before the copy engine's writes
+        // the warp's reads of this stage come before the copy engine's writes
+        if (ring.issued >= (uint32_t)G::kStages) fence_proxy_async_smem();
         mbar_arrive_expect_tx(&ring.full[s], G::kStageBytes);
         tma_load_3d(dst, &p.tm_k, &ring.full[s], 0, stage * kDec8Stage, pair, policy_evict_first());
         tma_load_3d(dst + G::kTile, &p.tm_v, &ring.full[s], 0, stage * kDec8Stage, pair, policy_evict_first());
@@ -722,14 +723,15 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
     volatile int* abort_flag = &abort_word;
     if (*abort_flag) return;
     // The whole list's length (every warp for itself).
-    int T = 0;
+    int T = 0, incl = 0;
     bool bad = false;
     Plan mine;
     for (int b = lane; b - lane < p.B; b += 32) {
         const uint32_t w = word_of(p, words, b);
         bad |= w == kBadLength;
         mine = Plan(p, w);
-        T += (int)__reduce_add_sync(0xffffffffu, mine.units()) * p.Hkv;
+        incl = warp_scan(mine.units()) * p.Hkv;
+        T += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.status, kStatusBadArgument);
     const Shares ctas(T, (int)gridDim.x);
@@ -743,8 +745,10 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
     if (left > 0) {
         int before = u_cta + sh.first(warp);  // units ahead of the share, less those of the sequences passed
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            if (p.B > 32) mine = Plan(p, word_of(p, words, b0 + lane));
-            const int incl = warp_scan(mine.units()) * p.Hkv;
+            if (p.B > 32) {  // else they are still here
+                mine = Plan(p, word_of(p, words, b0 + lane));
+                incl = warp_scan(mine.units()) * p.Hkv;
+            }
             const unsigned past = __ballot_sync(0xffffffffu, incl > before);
             if (past == 0) {
                 before -= __shfl_sync(0xffffffffu, incl, 31);
@@ -888,7 +892,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
     const Plan pl(p, s_word);
     if (p.selected && hk == 0 && r < p.n && tid == 0) p.selected[(long long)b * p.n + r] = sel ? 1 : 0;
     uint16_t* out = p.out + ((long long)pair * p.R + r) * D;
-    if (pl.len < p.n - tok) {  // the token lies before the sequence's start (or the length is invalid)
+    if (pl.len < p.n - tok) {  // the token lies before the sequence's start, or the length is invalid
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // no CTA ends ahead of the partial kernel
         for (int c = tid; c < D; c += (int)blockDim.x) out[c] = 0;
         return;
     }
