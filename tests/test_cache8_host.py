@@ -233,7 +233,8 @@ def test_every_unit_of_work_reaches_the_joining_kernel_once(seed):
     grid, warps = int(rng.choice([1, 5, 20, 148])), int(rng.choice([1, 3, 8, 12]))
     lens = rng.integers(0, Lmax + 1, B)
     plans = [plan(int(L), n, W, bool(rng.integers(0, 2)), Lmax) for L in lens]
-    units = [o + b - a for o, a, b in plans]
+    pads = [(b > a) + (o > 0) for o, a, b in plans]      # empty units behind a pair's stages
+    units = [o + b - a + e for (o, a, b), e in zip(plans, pads)]
     for L, (o, a, b) in zip(lens, plans):   # stages cover the window of every token, and all before it
         L = int(L)
         for i in range(max(0, n - L), n):
@@ -266,6 +267,8 @@ def test_every_unit_of_work_reaches_the_joining_kernel_once(seed):
                 runs[(pair, kind)] = (u, u + n_units)
                 run_of += [(pair, kind)] * n_units
                 u += n_units
+        run_of += [None] * pads[pair // Hkv]
+        u += pads[pair // Hkv]
     assert u == T
     written = {}                            # slot -> units whose states meet there
     for c in range(ctas[0]):
@@ -278,7 +281,9 @@ def test_every_unit_of_work_reaches_the_joining_kernel_once(seed):
         for w in range(inner[0]):
             mine = list(range(base + first(inner, w), base + first(inner, w + 1)))
             assert mine and all(of(ctas, x) == c and of(inner, x - base) == w for x in mine)
-            kinds = [run_of[x] for x in mine]
+            kinds = [run_of[x] for x in mine if run_of[x]]
+            if not kinds:
+                continue
             last[w] = kinds[-1]
             tails[w] = [x for x in mine if run_of[x] == kinds[-1]]
             for key in dict.fromkeys(kinds[:]):
@@ -288,6 +293,9 @@ def test_every_unit_of_work_reaches_the_joining_kernel_once(seed):
                     written[slot] = [x for x in mine if run_of[x] == key]
         w = 0
         while w < inner[0]:
+            if last[w] is None:
+                w += 1
+                continue
             v = w
             while v + 1 < inner[0] and last[v + 1] == last[w]:
                 v += 1
@@ -300,7 +308,8 @@ def test_every_unit_of_work_reaches_the_joining_kernel_once(seed):
         share = lambda c: cut(first(ctas, c + 1) - first(ctas, c), warps)  # noqa: E731
         v0, v1 = of(share(c0), a - first(ctas, c0)), of(share(c1), e - 1 - first(ctas, c1))
         slots = [c0 * warps + v0] + [c * warps for c in range(c0 + 1, c1 + 1)]
-        if first(share(c1), v1 + 1) != e - first(ctas, c1) and v1 != (v0 if c1 == c0 else 0):
+        behind = e + (pads[pair // Hkv] if kind == 0 else 0)
+        if first(share(c1), v1 + 1) > behind - first(ctas, c1) and v1 != (v0 if c1 == c0 else 0):
             slots.append(c1 * warps + v1)
         got = sum((written.pop((x + pair, kind)) for x in slots), [])
         assert sorted(got) == list(range(a, e))

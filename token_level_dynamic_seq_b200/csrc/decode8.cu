@@ -124,9 +124,13 @@ __device__ __forceinline__ uint32_t word_of(const Decode8Params& p, const uint32
     return b >= p.B ? 0u : b < kWordsMax ? words[b] : word_far(p, b);
 }
 
-// Units of one sequence: `out` stages before the window ([0, out), sequences with a
-// global token only), then stages [in0, in1).  They overlap in the stages that the
-// first window edges of the n tokens cross.
+// Units of one (sequence, key/value head): `out` stages before the window ([0, out),
+// sequences with a global token only), then stages [in0, in1); they overlap in the stages
+// that the first window edges of the n tokens cross.  Behind them lies one empty unit for
+// either kind that there is: beginning a run and writing its state takes a warp about as
+// long as a stage, and shares are equal in time where they count it (a batch of lengths 1
+// to 16384 in int8: the slowest warp, with nine runs, took 102,000 cycles against 82,000
+// for the others).
 struct Plan {
     int len;  // 0 also for an invalid length
     int out, in0, in1;
@@ -140,7 +144,8 @@ struct Plan {
         in1 = (len + kDec8Stage - 1) / kDec8Stage;
         out = (word & kGlobalBit) && e1 > 0 ? (e1 + kDec8Stage - 1) / kDec8Stage : 0;
     }
-    __device__ __forceinline__ int units() const { return out + in1 - in0; }
+    __device__ __forceinline__ int stages() const { return out + in1 - in0; }
+    __device__ __forceinline__ int units() const { return stages() + (len > 0 ? 1 : 0) + (out > 0 ? 1 : 0); }
 };
 
 __device__ __forceinline__ int warp_scan(int x)  // inclusive
@@ -394,15 +399,26 @@ __device__ __forceinline__ void join_states(const Decode8Params& p, const uint8_
 
 // Where in the list a warp's copies are: unit `off` of key/value head hk of sequence b.
 struct Cursor {
-    int b, hk, off, units;
+    int b, hk, off;
     Plan pl;
+    // To the next pair's first unit.
+    __device__ __forceinline__ void next_pair(const Decode8Params& p, const uint32_t* words)
+    {
+        off = 0;
+        if (++hk < p.Hkv) return;
+        hk = 0;
+        do {
+            if (++b >= p.B) return;
+            pl = Plan(p, word_of(p, words, b));
+        } while (pl.len == 0);
+    }
 };
 
 // The next unit's keys and values into the ring (all lanes keep count, lane 0 copies), and
 // beside them what the warp has to know of the stage: the run (2 pair + kind), the stage's
 // index in the sequence and the sequence's length.
 template <int D, int NT>
-__device__ __forceinline__ void issue_unit(const Decode8Params& p, const uint32_t* words, Ring8& ring, int4* units, Cursor& at)
+__device__ __forceinline__ void issue_unit(const Decode8Params& p, Ring8& ring, int4* units, Cursor& at)
 {
     using G = D8<D, NT>;
     const bool inside = at.off >= at.pl.out;
@@ -418,15 +434,7 @@ __device__ __forceinline__ void issue_unit(const Decode8Params& p, const uint32_
         units[s] = make_int4(2 * pair + (inside ? 0 : 1), stage, at.pl.len, 0);
     }
     ++ring.issued;
-    if (++at.off < at.units) return;
-    at.off = 0;
-    if (++at.hk < p.Hkv) return;
-    at.hk = 0;
-    do {
-        if (++at.b >= p.B) return;
-        at.pl = Plan(p, word_of(p, words, at.b));
-        at.units = at.pl.units();
-    } while (at.units == 0);
+    ++at.off;
 }
 
 // Per-lane constants of the (sequence, key/value head) at hand.
@@ -740,9 +748,9 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
     const int u_cta = ctas.first(cta);
     const Shares sh(ctas.first(cta + 1) - u_cta, G::kWarps);
     const int gw = cta * G::kWarps + warp;
-    int left = warp < sh.N ? sh.first(warp + 1) - sh.first(warp) : 0;
+    int to_issue = warp < sh.N ? sh.first(warp + 1) - sh.first(warp) : 0;
     Cursor at{};
-    if (left > 0) {
+    if (to_issue > 0) {
         int before = u_cta + sh.first(warp);  // units ahead of the share, less those of the sequences passed
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             if (p.B > 32) {  // else they are still here
@@ -760,17 +768,17 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
             at.pl.out = __shfl_sync(0xffffffffu, mine.out, src);
             at.pl.in0 = __shfl_sync(0xffffffffu, mine.in0, src);
             at.pl.in1 = __shfl_sync(0xffffffffu, mine.in1, src);
-            at.units = at.pl.units();
-            before -= __shfl_sync(0xffffffffu, incl, src) - at.units * p.Hkv;
-            at.hk = (int)((unsigned)before / (unsigned)at.units);
-            at.off = before - at.hk * at.units;
+            const int units = at.pl.units();
+            before -= __shfl_sync(0xffffffffu, incl, src) - units * p.Hkv;
+            at.hk = (int)((unsigned)before / (unsigned)units);
+            at.off = before - at.hk * units;
             break;
         }
     }
     const uint32_t base = ((smem_u32(dsmem8) + 1023u) & ~1023u) + warp * G::kWarpBytes;
     uint2* qs = reinterpret_cast<uint2*>(__cvta_shared_to_generic(base + G::kRingBytes));
     Ring8 ring{base, full_bars[warp], 0, 0};
-    int to_issue = left, run = -1, lo0 = 0, hi0 = 0, first = 0, last = 0;
+    int run = -1, lo0 = 0, hi0 = 0, first = 0, last = 0;
     float ks32 = 0.f, vs32 = 0.f;  // scales of stages first .. first + 31, one per lane
     bool ok = true;
     Rows8<NT> rw;
@@ -785,14 +793,20 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
     st.init();
     for (;;) {
         while (to_issue > 0 && ring.issued - ring.used < (uint32_t)G::kStages) {
-            issue_unit<D, NT>(p, words, ring, unit_info[warp], at);
+            if (at.off >= at.pl.stages()) {  // the empty units at a pair's end
+                to_issue -= at.pl.units() - at.off;
+                at.next_pair(p, words);
+                continue;
+            }
+            issue_unit<D, NT>(p, ring, unit_info[warp], at);
             --to_issue;
         }
         __syncwarp();
         const uint32_t s = ring.used % G::kStages;
-        const int4 unit = left > 0 ? unit_info[warp][s] : make_int4(-1, 0, 0, 0);
-        if (unit.x != run || left == 0) {
-            if (left == 0) break;  // the share's last state stays in registers
+        const bool done = ring.used == ring.issued;
+        const int4 unit = done ? make_int4(-1, 0, 0, 0) : unit_info[warp][s];
+        if (unit.x != run || done) {
+            if (done) break;       // the share's last state stays in registers
             if (run >= 0) {        // a run ends inside the share: its state goes to its slot
                 const long long row = row_at(p, gw, run >> 1, run & 1);
                 store_state8<D, NT>(st, p.R, part_ml(p) + row, part_o(p) + row * D);
@@ -824,7 +838,6 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
         const bool masked = pos0 < lo0 + p.n - 1 || pos0 + kDec8Stage - 1 > hi0;
         do_stage<TYPE, D, NT>(st, rw, qs, ring.base + s * G::kStageBytes, ks, vs, masked, pos0, lo0, hi0, p.n);
         ++ring.used;
-        --left;
         __syncwarp();  // every lane is done with the stage
     }
     if (!ok) {
@@ -901,7 +914,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
     // first warp there; and the run's last warp's own where its share goes on behind the run.
     const Shares ctas(T, grid);
     const int u0 = before + hk * pl.units();
-    const int from[2] = {u0 + pl.out, u0}, to[2] = {u0 + pl.units(), u0 + (sel ? pl.out : 0)};
+    const int from[2] = {u0 + pl.out, u0}, to[2] = {u0 + pl.stages(), u0 + (sel ? pl.out : 0)};
     int cnt[2], extra[2];
     long long row0[2], row1[2], row_x[2];
     #pragma unroll
@@ -916,7 +929,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
         cnt[k] = c1 - c0 + 1;
         row0[k] = row_at(p, c0 * kWarps + v0, pair, k) + r;      // in the first CTA
         row1[k] = row_at(p, (c0 + 1) * kWarps, pair, k) + r;     // in the next, kWarps slots from one to the next
-        extra[k] = s1.first(v1 + 1) != to[k] - ctas.first(c1) && v1 != (c1 == c0 ? v0 : 0);
+        // (the empty units behind a pair's last run are no other run)
+        const int behind = k == 0 ? u0 + pl.units() : to[k];
+        extra[k] = s1.first(v1 + 1) > behind - ctas.first(c1) && v1 != (c1 == c0 ? v0 : 0);
         row_x[k] = row_at(p, c1 * kWarps + v1, pair, k) + r;
     }
     const float2* ml = part_ml(p);
