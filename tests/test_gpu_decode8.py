@@ -183,6 +183,35 @@ def test_values_that_are_not_finite_stay_where_they_are_seen(n):
         assert ((out[0].double() - want).abs() <= bound)[~bad].all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_queries_keys_and_scales_that_are_not_finite(dtype):
+    """A NaN query makes its own row NaN and no other; a NaN scale, every row that sees the block; all keys NaN, all."""
+    cache, model, gen = build(2, 1, 700, 64, dtype, 64, [700, 130], seed=9)
+    lens, tau = [700, 130], 0.0
+    q, gate = torch.randn(2, 3, 2, 64, generator=gen).bfloat16(), torch.full((2, 2), 1.0)
+    q[0, 1, 0, 5] = float("nan")
+    q[1, 2, 1, 0] = float("inf")
+    ws = logo.decode8_workspace(cache, 3, 2)
+    go_ = lambda g=gate, W=100: logo.decode8(q.cuda(), cache, ints(lens), g.cuda(), torch.tensor([tau], device="cuda"),  # noqa: E731
+                                             W, ws=ws)[0].float().cpu()
+    out = go_()
+    bad = torch.isnan(out).any(-1)
+    want = torch.zeros(2, 3, 2, dtype=torch.bool)
+    want[0, 1, 0] = want[1, 2, 1] = True
+    assert torch.equal(bad, want)
+    for b in range(2):
+        ref_out, bound = ref.decode(q[b], model.values("k", b), model.values("v", b), gate[b], tau, 100)
+        ok = ~want[b]
+        assert ((out[b].double() - ref_out).abs() <= bound)[ok].all()
+    cache.k_scale[0, 0, 3] = float("nan")        # positions 192 .. 255 of sequence 0: behind the window of 100
+    assert torch.isnan(go_()[0]).all()           # global rows see them
+    quiet = torch.full((2, 2), -1.0)
+    assert torch.equal(torch.isnan(go_(quiet)).any(-1), want)
+    cache.k_scale[0] = float("nan")
+    assert torch.isnan(go_(quiet)[0]).all() and torch.equal(torch.isnan(go_(quiet)[1]).any(-1), want[1])
+    logo.check(ws)
+
+
 def test_gates_thresholds_and_row_behind_short_sequences():
     cache, model, gen = build(4, 2, 300, 64, torch.int8, 64, [300, 300, 300, 1], seed=2)
     nan, inf = float("nan"), float("inf")

@@ -70,9 +70,6 @@ namespace {
 #ifndef LOGO_DEC8_RING
 #define LOGO_DEC8_RING 16384
 #endif
-#ifndef LOGO_DEC8_UG
-#define LOGO_DEC8_UG 2
-#endif
 constexpr float kPBias = 15.f;  // P is held times 2^15: the state's m is the maximum less 15
 constexpr int kWordsMax = 1024; // sequences whose length and gate decision a CTA keeps in shared memory
 
@@ -675,7 +672,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
     }
     if (TYPE == kCacheInt8) vs *= kInt8Unit;
     const uint32_t vat = swz<D>(tileV, lane, 0);
-    constexpr int UG = LOGO_DEC8_UG;  // column groups of 16 in flight
+    constexpr int UG = 2;  // column groups of 16 in flight
     #pragma unroll
     for (int u0 = 0; u0 < D / 16; u0 += UG) {
         uint32_t ev[UG][4], od[UG][4];
@@ -941,8 +938,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
         return i == 0 ? row0[k] : i < cnt[k] ? row1[k] + (i - 1) * step : row_x[k];
     };
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // Each warp joins its states four at a time, all of their loads in flight together; then
+    // Each warp joins its states kJoin at a time, all of their loads in flight together; then
     // warp 0 joins the warps'.
+    constexpr int kJoin = 8;
     float m[2], l[2], o[2][C];
     #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -959,37 +957,49 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
             v[0] = x.x, v[1] = x.y;
         }
     };
-    auto join = [&](int k, float mi, float li, const float (&v)[C]) {
-        const float mn = fmaxf(m[k], mi);
-        const float f0 = m[k] == -INFINITY ? 0.f : exp2f(m[k] - mn), f1 = mi == -INFINITY ? 0.f : exp2f(mi - mn);
-        m[k] = mn;
-        l[k] = fmaf(f0, l[k], f1 * li);
-        #pragma unroll
-        for (int c = 0; c < C; ++c) o[k][c] = fmaf(f0, o[k][c], f1 * v[c]);
-    };
+    // weight of a state with maximum x among those with maximum y >= x
+    auto weight = [](float x, float y) { return x == -INFINITY ? 0.f : fast_exp2(x - y); };
     const int all = cnt[0] + extra[0] + cnt[1] + extra[1];
     #pragma unroll 1
-    for (int i0 = warp; i0 < all; i0 += 4 * nw) {
-        float2 s[4];
-        float v[4][C];
-        int kind[4];
+    for (int i0 = warp; i0 < all; i0 += kJoin * nw) {
+        float2 s[kJoin];
+        float v[kJoin][C];
+        bool outside[kJoin];
+        float mx[2] = {m[0], m[1]};
         #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kJoin; ++j) {
             const int i = i0 + j * nw;
-            kind[j] = i >= cnt[0] + extra[0];
+            outside[j] = i >= cnt[0] + extra[0];
             s[j] = make_float2(-INFINITY, 0.f);
             #pragma unroll
             for (int c = 0; c < C; ++c) v[j][c] = 0.f;
             if (i < all) {
-                const long long row = kind[j] ? row_of(1, i - cnt[0] - extra[0]) : row_of(0, i);
+                const long long row = outside[j] ? row_of(1, i - cnt[0] - extra[0]) : row_of(0, i);
                 s[j] = ml[row];
                 load(po + row * D, v[j]);
             }
         }
         #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (kind[j]) join(1, s[j].x, s[j].y, v[j]);
-            else join(0, s[j].x, s[j].y, v[j]);
+        for (int j = 0; j < kJoin; ++j) {
+            mx[0] = fmaxf(mx[0], outside[j] ? -INFINITY : s[j].x);
+            mx[1] = fmaxf(mx[1], outside[j] ? s[j].x : -INFINITY);
+        }
+        #pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float f = weight(m[k], mx[k]);
+            m[k] = mx[k];
+            l[k] *= f;
+            #pragma unroll
+            for (int c = 0; c < C; ++c) o[k][c] *= f;
+            #pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+                // (a weight of zero does not hide a state that is NaN)
+                const bool here = outside[j] == (k == 1);
+                const float w = weight(s[j].x, mx[k]);
+                l[k] = here ? fmaf(w, s[j].y, l[k]) : l[k];
+                #pragma unroll
+                for (int c = 0; c < C; ++c) o[k][c] = here ? fmaf(w, v[j][c], o[k][c]) : o[k][c];
+            }
         }
     }
     if (nw > 1) {
@@ -1001,14 +1011,24 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
         }
         __syncthreads();
         if (warp > 0) return;
-        #pragma unroll 1
-        for (int w = 1; w < nw; ++w)
+        #pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float mx = m[k];
+            for (int w = 1; w < nw; ++w) mx = fmaxf(mx, red_m[k][w]);
+            const float f = weight(m[k], mx);
+            m[k] = mx;
+            l[k] *= f;
             #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int c = 0; c < C; ++c) o[k][c] *= f;
+            for (int w = 1; w < nw; ++w) {
                 float v[C];
                 load(&red_o[k][w][lane * C], v);
-                join(k, red_m[k][w], red_l[k][w], v);
+                const float g = weight(red_m[k][w], mx);
+                l[k] = fmaf(g, red_l[k][w], l[k]);
+                #pragma unroll
+                for (int c = 0; c < C; ++c) o[k][c] = fmaf(g, v[c], o[k][c]);
             }
+        }
     }
     float val[C];
     #pragma unroll
