@@ -46,12 +46,9 @@ cudaError_t launch_append8(const Append8Params& p, int type, int d, int block, c
 cudaError_t launch_read8(const Read8Params& p, int type, int d, int block, cudaStream_t stream);
 
 // Decode over the cache (decode8.cu).
-#ifndef LOGO_DEC8_POS
-#define LOGO_DEC8_POS 32
-#endif
-constexpr int kDec8Stage = LOGO_DEC8_POS;  // cache positions per staged unit; every scale block is a multiple of it
+constexpr int kDec8Stage = 32;        // cache positions per staged unit; every scale block is a multiple of it
 constexpr int kDec8MaxRows = 32;      // query rows (heads of a group x new tokens) of one key/value head
-constexpr int kDec8MaxWarps = 1776;   // warps that a launch spreads the work over, at most (148 SMs x 12)
+constexpr int kDec8MaxWarps = 1184;   // warps that a launch spreads the work over, at most (148 SMs x 8)
 
 struct alignas(64) Decode8Params {
     CUtensorMap tm_k, tm_v;     // codes as [B*Hkv][Lmax][d] bytes, box d x kDec8Stage x 1, swizzled rows

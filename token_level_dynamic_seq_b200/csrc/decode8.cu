@@ -58,18 +58,6 @@ namespace logo {
 
 namespace {
 
-#ifndef LOGO_DEC8_WARPS1
-#define LOGO_DEC8_WARPS1 8
-#endif
-#ifndef LOGO_DEC8_WARPS2
-#define LOGO_DEC8_WARPS2 8
-#endif
-#ifndef LOGO_DEC8_WARPS4
-#define LOGO_DEC8_WARPS4 6
-#endif
-#ifndef LOGO_DEC8_RING
-#define LOGO_DEC8_RING 16384
-#endif
 constexpr float kPBias = 15.f;  // P is held times 2^15: the state's m is the maximum less 15
 constexpr int kWordsMax = 1024; // sequences whose length and gate decision a CTA keeps in shared memory
 
@@ -77,13 +65,16 @@ template <int D, int NT>
 struct D8 {
     static constexpr int kTile = kDec8Stage * D;                  // codes of K (or V) of one stage, bytes
     static constexpr int kStageBytes = 2 * kTile;                 // K then V
-    static constexpr int kRingBytes = LOGO_DEC8_RING;
+    static constexpr int kRingBytes = 16384;                      // of a warp; 128 KB in flight on an SM
     static constexpr int kStages = kRingBytes / kStageBytes;      // ring depth
     static constexpr int kQBytes = (D / 16) * NT * 32 * 8;        // q fragments of one warp
     static constexpr int kStateBytes = 8 * NT * (D + 2) * 4;      // partial state, written over the ring at the end
     static constexpr int kUsedBytes = kRingBytes + kQBytes > kStateBytes ? kRingBytes + kQBytes : kStateBytes;
     static constexpr int kWarpBytes = (kUsedBytes + 1023) / 1024 * 1024;
-    static constexpr int kWarps = NT == 1 ? LOGO_DEC8_WARPS1 : NT == 2 ? LOGO_DEC8_WARPS2 : LOGO_DEC8_WARPS4;
+    // Two warps on every scheduler, and registers and shared memory left for the combine
+    // kernel's CTAs (12 warps: they wait for the others to end, 10.4 -> 13.9 us for short
+    // contexts, 21.0 -> 25.0 us for one of 32K); six where 32 rows of O fill the registers.
+    static constexpr int kWarps = NT == 4 && D == 128 ? 6 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSmem = kWarps * kWarpBytes + 1024;      // + alignment slack
     static constexpr int MT = kDec8Stage / 16;                    // 16-position tiles of a stage

@@ -160,7 +160,7 @@ def cache8_read(cache: Cache8, start, rows: int, ws=None, cu_seqlens=None, max_s
     rows = int(rows)
     want = (cache.B if cu_seqlens is None else 1, cache.Hkv, rows, cache.d)
     if out is None:
-        out = cache.k_tail.new_empty(want), cache.k_tail.new_empty(want)
+        out = cache.k_tail.new_empty((2,) + want).unbind(0)
         _used_on(stream, *out)
     k, v = out
     if tuple(k.shape) != want or tuple(v.shape) != want:
