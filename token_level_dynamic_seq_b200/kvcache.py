@@ -186,11 +186,11 @@ def decode8(q, cache: Cache8, cache_len, gate, tau, window: int, ws=None, scale:
             stream=None):
     """Decode step over the cache: ``q`` bf16 [B, Hq, n, d] (or [B, Hq, d] for one token), ``cache_len`` int32 [B]
     (the new tokens included), ``gate`` fp32 [B, n], ``tau`` fp32 [1].  Returns (out, like q; selected int32 [B, n])."""
-    if q.dim() not in (3, 4) or q.shape[0] != cache.B or q.shape[-1] != cache.d:
+    B, Hq, *n, d = q.shape
+    if len(n) > 1 or B != cache.B or d != cache.d:
         raise ValueError(f"q: expected [{cache.B}, Hq, n, {cache.d}], got {tuple(q.shape)}")
+    n = n[0] if n else 1
     lib = _lib_on(cache)
-    B, Hq = cache.B, q.shape[1]
-    n = q.shape[2] if q.dim() == 4 else 1
     if ws is None:
         ws = decode8_workspace(cache, Hq, n, stream)
     if out is None:
