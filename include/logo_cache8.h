@@ -67,7 +67,7 @@ typedef struct {
  *            or, where the sequence's latest append went from s to e, a position
  *            from s to e whose block is one of the last two up to e.  Positions
  *            behind the new rows are given up.
- *   new_len  int32 [B] (device) receiving start[b] + n_b, or NULL; not start itself.
+ *   new_len  int32 [B] (device) receiving start[b] + n_b, or NULL; apart from start.
  * k and v must be 32-byte aligned.  A sequence whose rows do not fit (start < 0
  * or start + n_b > Lmax), or whose packed offsets are out of order, beyond T or
  * longer than max_seqlen, is left as it is (new_len = start) and reported:

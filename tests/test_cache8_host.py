@@ -94,6 +94,8 @@ def test_append_refuses_tails_and_new_len():
     assert append(lib, desc(v_tail=(1 << 20) + 16)) == 1
     assert append(lib, desc(), new_len=FAKE) == 1                    # the same array as start
     assert append(lib, desc(), new_len=ctypes.c_void_p((2 << 20) + 1)) == 1
+    assert append(lib, desc(), new_len=ctypes.c_void_p((1 << 20) + 4)) == 1   # one element of the two shared
+    assert append(lib, desc(), new_len=ctypes.c_void_p((1 << 20) - 4)) == 1
 
 
 @no_gpu_only

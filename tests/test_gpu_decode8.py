@@ -110,7 +110,7 @@ def test_long_caches(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("size", [1e-30, 1e30])
+@pytest.mark.parametrize("size", [1e-30, 1e30, 2e37])
 def test_blocks_of_very_different_scales(dtype, size):
     """Values whose blocks differ by 60 orders of magnitude: the small ones count where the large ones are not seen.
     Keys and queries far from one with a scale that makes up for it."""
@@ -124,6 +124,32 @@ def test_blocks_of_very_different_scales(dtype, size):
     fill(cache, model, k.bfloat16(), v.bfloat16(), [0, L, 2 * L], [L, L])
     go(cache, model, gen, 2, 1, 100, [L, L], tau=10.0, scale=1e4 / 8, qsize=1e8)
     go(cache, model, gen, 2, 1, 100, [L, L], tau=-10.0, scale=1e4 / 8, qsize=1e8)
+
+
+@pytest.mark.parametrize("n", [1, 2])
+def test_more_sequences_than_a_cta_keeps_lengths_of(n):
+    """1,300 sequences: the lengths of the last ones are read from memory again wherever they are needed."""
+    lens = [(i * 53) % 97 for i in range(1300)]
+    cache, model, gen = build(1300, 1, 97, 64, torch.int8, 64, lens, seed=4)
+    go(cache, model, gen, 2, n, 40, lens)
+
+
+def test_two_streams_with_a_workspace_each():
+    """Two batches decoded at the same time on two streams give what each gives alone."""
+    made = [build(2, 2, 3000, 128, t, 64, [3000, 1700], seed=30 + i) for i, t in enumerate(TYPES)]
+    runs = []
+    for cache, model, gen in made:
+        q, gate = torch.randn(2, 8, 1, 128, generator=gen).bfloat16().cuda(), torch.randn(2, 1, generator=gen).cuda()
+        runs.append((q, cache, ints([3000, 1700]), gate, torch.tensor([0.0], device="cuda"), 500,
+                     logo.decode8_workspace(cache, 8)))
+    alone = [logo.decode8(*r)[0] for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(20):
+        outs = [logo.decode8(*r, stream=s)[0] for r, s in zip(runs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, outs):
+            assert torch.equal(a, b)
 
 
 def test_peaked_scores_and_long_tails_of_small_weights():

@@ -859,7 +859,9 @@ logo_status logo_cache8_append(const logo_cache8* cache, const logo_bf16* k, con
         return st;
     if (g.L > 0 && ((st = check_ptr(k, "k", 32)) != LOGO_OK || (st = check_ptr(v, "v", 32)) != LOGO_OK)) return st;
     if (new_len && (st = check_ptr(new_len, "new_len", 4)) != LOGO_OK) return st;
-    if (new_len == start) return fail(LOGO_ERR_INVALID_ARG, "new_len must not be start");
+    // Every CTA reads start while one writes new_len.
+    if (new_len && new_len < start + cache->B && start < new_len + cache->B)
+        return fail(LOGO_ERR_INVALID_ARG, "new_len overlaps start");
     logo::Append8Params p;
     memset(&p, 0, sizeof p);
     p.c = view_of(cache);

@@ -243,6 +243,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 // Codes as fp16 pairs, exact.  e4m3: the code's value.  int8: (code + 128) 2^-24, a subnormal number whose bits are the code's with the sign bit turned; the
 // products' accumulators start at -128 2^-24 times the other operand's sum instead of zero.
 constexpr uint32_t kOnes = 0x3c003c00u;  // two fp16 ones
+// P's 2^15 and the codes' 2^-24 would take O out of range for values beyond 1e34: O is kept
+// without them, and the state's l is given the same factor when it is written.
+template <int TYPE>
+constexpr float kVScale = TYPE == kCacheE4M3 ? 1.f / 32768.f : 1.f;
+template <int TYPE>
+constexpr float kLScale = TYPE == kCacheE4M3 ? 1.f / 32768.f : 1.f / 16777216.f;
 constexpr float kInt8Unit = 16777216.f, kInt8Shift = -128.f / 16777216.f;
 
 template <int TYPE>
@@ -328,7 +334,7 @@ __device__ __forceinline__ void store_if(bool yes, void* at, float a, float b)
 // The state's rows to (m, l) at ml[r] and o at o[r * D], in shared or global memory.  Predicated
 // stores and no branches: this code runs once or twice in a launch, and every branch of it
 // would wait for its instructions.
-template <int D, int NT>
+template <int TYPE, int D, int NT>
 __device__ __forceinline__ void store_state8(State8<D, NT>& st, int R, float2* ml, float* o)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -343,7 +349,7 @@ __device__ __forceinline__ void store_state8(State8<D, NT>& st, int R, float2* m
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int r = 8 * nt + 2 * t + c;
-            store_if(r < R && g == 0, ml + r, st.m[nt][c], st.l[nt][c]);
+            store_if(r < R && g == 0, ml + r, st.m[nt][c], st.l[nt][c] * kLScale<TYPE>);
             float* row = o + r * D + 2 * g;
             #pragma unroll
             for (int u = 0; u < D / 16; ++u)
@@ -661,7 +667,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
             o0[nt][1] = ones[1] * kInt8Shift;
         }
     }
-    if (TYPE == kCacheInt8) vs *= kInt8Unit;
+    vs *= kVScale<TYPE>;
     const uint32_t vat = swz<D>(tileV, lane, 0);
     constexpr int UG = 2;  // column groups of 16 in flight
     #pragma unroll
@@ -797,7 +803,7 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
             if (done) break;       // the share's last state stays in registers
             if (run >= 0) {        // a run ends inside the share: its state goes to its slot
                 const long long row = row_at(p, gw, run >> 1, run & 1);
-                store_state8<D, NT>(st, p.R, part_ml(p) + row, part_o(p) + row * D);
+                store_state8<TYPE, D, NT>(st, p.R, part_ml(p) + row, part_o(p) + row * D);
             }
             // token i sees [lo0 + i, hi0 + i]: its window, or what lies before it (lo0 then at
             // most 0 for every token)
@@ -846,7 +852,7 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
         while (hi + 1 < G::kWarps && last_run[hi + 1] == run) ++hi;
         const long long row = row_at(p, gw, run >> 1, run & 1);
         float* own = reinterpret_cast<float*>(__cvta_shared_to_generic(base));  // over the ring
-        store_state8<D, NT>(st, p.R, lo == hi ? part_ml(p) + row : reinterpret_cast<float2*>(own + 8 * NT * D),
+        store_state8<TYPE, D, NT>(st, p.R, lo == hi ? part_ml(p) + row : reinterpret_cast<float2*>(own + 8 * NT * D),
                             lo == hi ? part_o(p) + row * D : own);
     }
     __syncthreads();
