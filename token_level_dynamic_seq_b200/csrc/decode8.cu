@@ -10,14 +10,14 @@
 //
 // Bound by HBM: one byte per element of the cache read, about 2 R FLOP per byte for
 // the R = (Hq / Hkv) n query rows that share a key/value head.
-//   decode8_partial_kernel  one wave of persistent warps.  The work is a list of
-//     units: for every (sequence, key/value head) the 64-position stages before the
-//     window (only where a token is global), then the stages that reach into it.
-//     The list is cut into equal shares, one per warp, so every warp reads the same
-//     number of bytes whatever the lengths and gates are; the lengths are read on the
-//     device.  A warp streams its stages through a private ring in shared memory,
-//     filled by TMA (rows swizzled), tracked by one mbarrier per stage and kept full
-//     from one sequence to the next.  Per stage:
+//   decode8_partial_kernel  one wave of persistent warps, 8 to an SM.  The work is a
+//     list of units: for every (sequence, key/value head) the 32-position stages before
+//     the window (only where a token is global), then the stages that reach into it.
+//     The list is cut into equal shares, one per warp, so every warp reads about the
+//     same number of bytes whatever the lengths and gates are; the lengths are read on
+//     the device.  A warp streams its stages through a private ring of 16 KB in shared
+//     memory, filled by TMA (rows swizzled), tracked by one mbarrier per stage and kept
+//     full from one sequence to the next.  Per stage:
 //       S^T = K q^T   mma.sync m16n8k16, fp16 in, fp32 out: positions are the rows,
 //                     the query rows the columns.  Codes become fp16 exactly.  The
 //                     order of the head dimension inside a product is free, so a lane
@@ -27,22 +27,36 @@
 //       O^T += V^T P^T  V^T by ldmatrix.trans on pairs of codes: a word holds two
 //                     head-dimension columns at two positions, and one byte permute
 //                     sorts it into the fp16 pairs of two rows of V^T.  Each stage's
-//                     product starts from zero and joins O with the stage's V scale in
+//                     product starts anew and joins O with the stage's V scale in
 //                     fp32, so scales of any ratio meet only in 32 bits.
 //     Positions outside the window and inside it go to separate partial states
 //     (m, l, o): a position is read once, local attention is the inside state, global
-//     attention both.
-//   decode8_combine_kernel  one CTA per query row: joins the states of the warps that
-//     held a share of the row's stages; o = local + sigmoid(g) * global, one rounding.
+//     attention both.  The warps of a CTA join their states in shared memory.
+//   decode8_combine_kernel  one CTA per query row, placed while the first kernel runs:
+//     joins the states of the CTAs that held a share of the row's stages, in the order of
+//     the list; o = local + sigmoid(g) * global, one rounding.
 //
-// mma.sync and not tcgen05: a stage of 16 KB takes an SM about 700 cycles to fetch and
-// its 64 products a fraction of that, and codes need a conversion in registers, which
-// an operand read from shared memory by tcgen05 would not see.
+// mma.sync and not tcgen05: a stage of 8 KB takes an SM about 350 cycles to fetch and its
+// 32 products a fraction of that, and codes need a conversion in registers, which an
+// operand read from shared memory by tcgen05 would not see.
 //
 // Roundings: q is scaled by a power of two per row, so that its largest element lies
 // in [2^14, 2^15), and rounded to fp16 (exact for elements down to 2^-28 of the
 // largest).  P is 2^15 exp2(s - m) in fp16: 11 bits, 3 more than bf16, with values
 // down to 2^-39 of the largest kept.  The sum l uses the unrounded P.
+//
+// Measured (d = 128, 32 query heads on 8, e4m3, window 4096; bytes that have to be read
+// over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 214 us (0.92);
+// one global sequence of 128K beside a local one 50 us (0.84); one of 32K 19.6 us (0.52);
+// 16 of 8K to 32K with four drafted tokens each 63 us (0.64); two of 4K 9.5 us.  Once its
+// first bytes are there (5 us: launch, lengths, the first 19 MB of all SMs' rings), a warp
+// takes 2,650 to 3,000 cycles a stage, of which HBM alone asks 2,850; the kernel's end and
+// the combine take 4 us.  With several drafts the issue of a stage's 770 instructions
+// (530 for one token) is as long as its fetch.
+// Tried and left out: 64-position stages (more instructions a warp in a row: 16 drafts
+// batch 70 us), paired fp32 instructions for the state (register moves: 72 us), chunks of
+// the list's end fetched by a counter (64 sequences 220 us), rows finished by the last CTA
+// of a pair instead of a second kernel (drafts 86 us), q fetched ahead (no change).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
