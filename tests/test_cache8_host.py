@@ -14,7 +14,6 @@ import torch
 import token_level_dynamic_seq_b200 as logo
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-STAGE = 32   # positions of a unit of work
 FAKE, FAKE2 = ctypes.c_void_p(1 << 20), ctypes.c_void_p(2 << 20)
 no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(),
                                  reason="placeholder pointers are only passed where no GPU exists")
@@ -115,7 +114,7 @@ def test_workspace_size():
     size = lambda c, Hq, n: lib.logo_decode8_workspace_size(by(c), Hq, n)  # noqa: E731
     one = size(desc(k=None), 8, 1)      # the buffers need not exist yet
     assert one > 256 and size(desc(), 8, 4) > one and size(desc(), 16, 1) > one
-    assert one == 256 + (1184 + 4) * 2 * 4 * 130 * 4
+    assert one == 256 + 64 * 4 + (1184 + 4) * 2 * 4 * 130 * 4
     for c, Hq, n in ((None, 8, 1), (desc(d=32), 8, 1), (desc(), 0, 1), (desc(), 8, 0), (desc(), 8, 9), (desc(), 5, 1)):
         assert size(c, Hq, n) == 0
 
@@ -216,7 +215,7 @@ def test_snapped_product_rounds_as_the_exact_quotient(top):
 
 # ---------------------------------------------------------------- division of the decode's work
 
-def plan(length, n, W, any_global, Lmax):
+def plan(length, n, W, any_global, Lmax, STAGE):
     """Units of one sequence as the kernel counts them: (out, in0, in1)."""
     if length <= 0 or length > Lmax:
         return 0, 0, 0
@@ -234,7 +233,8 @@ def test_every_unit_of_work_reaches_the_joining_kernel_once(seed):
     W = min(int(rng.integers(1, 6000)), Lmax)
     grid, warps = int(rng.choice([1, 5, 20, 148])), int(rng.choice([1, 3, 6, 8]))
     lens = rng.integers(0, Lmax + 1, B)
-    plans = [plan(int(L), n, W, bool(rng.integers(0, 2)), Lmax) for L in lens]
+    STAGE = int(rng.choice([32, 64]))   # positions of a unit, for d = 128 and 64
+    plans = [plan(int(L), n, W, bool(rng.integers(0, 2)), Lmax, STAGE) for L in lens]
     pads = [(b > a) + (o > 0) for o, a, b in plans]      # empty units behind a pair's stages
     units = [o + b - a + e for (o, a, b), e in zip(plans, pads)]
     for L, (o, a, b) in zip(lens, plans):   # stages cover the window of every token, and all before it

@@ -439,7 +439,7 @@ logo::Cache8View view_of(const logo_cache8* c)
     return v;
 }
 
-// Codes as bytes [slabs][rows][d], box d x kDec8Stage x 1, swizzled over the whole row.
+// Codes as bytes [slabs][rows][d], box d x dec8_stage(d) x 1, swizzled over the whole row.
 logo_status make_map8(CUtensorMap* map, const void* base, int d, int rows, int slabs)
 {
     logo_status st;
@@ -447,7 +447,7 @@ logo_status make_map8(CUtensorMap* map, const void* base, int d, int rows, int s
     if (!fn) return st;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)slabs};
     cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)d * (cuuint64_t)rows};
-    cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)logo::kDec8Stage, 1};
+    cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)logo::dec8_stage(d), 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -945,7 +945,7 @@ logo_status logo_decode8(const logo_bf16* q, const logo_cache8* cache, const int
     p.Lmax = cache->Lmax;
     p.W = window < cache->Lmax ? window : cache->Lmax;
     p.nblk = (cache->Lmax + cache->block - 1) / cache->block;
-    p.block_units = cache->block / logo::kDec8Stage;
+    p.block = cache->block;
     p.scale_log2 = sl2;
     p.timeout_ns = 1000000000ull;  // 1 s per wait: far above any legitimate stall
     NvtxRange range("logo decode, 8-bit cache");

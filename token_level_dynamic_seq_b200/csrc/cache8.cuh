@@ -46,12 +46,14 @@ cudaError_t launch_append8(const Append8Params& p, int type, int d, int block, c
 cudaError_t launch_read8(const Read8Params& p, int type, int d, int block, cudaStream_t stream);
 
 // Decode over the cache (decode8.cu).
-constexpr int kDec8Stage = 32;        // cache positions per staged unit; every scale block is a multiple of it
+// Cache positions per staged unit: 4 KB of K and as much of V.  Every scale block is a
+// multiple of it.
+__host__ __device__ constexpr int dec8_stage(int d) { return 4096 / d; }
 constexpr int kDec8MaxRows = 32;      // query rows (heads of a group x new tokens) of one key/value head
 constexpr int kDec8MaxWarps = 1184;   // warps that a launch spreads the work over, at most (148 SMs x 8)
 
 struct alignas(64) Decode8Params {
-    CUtensorMap tm_k, tm_v;     // codes as [B*Hkv][Lmax][d] bytes, box d x kDec8Stage x 1, swizzled rows
+    CUtensorMap tm_k, tm_v;     // codes as [B*Hkv][Lmax][d] bytes, box d x dec8_stage(d) x 1, swizzled rows
     const uint16_t* q;          // [B, Hq, n, d]
     const float *k_scale, *v_scale;
     const int32_t* cache_len;   // [B], the new tokens included
@@ -59,10 +61,11 @@ struct alignas(64) Decode8Params {
     const float* tau;           // one threshold (device)
     uint16_t* out;              // [B, Hq, n, d]
     int32_t* selected;          // [B, n] or nullptr
-    float* part;                // partial states in the workspace
+    float* part;                // the workspace behind its header
     uint32_t* status;
     int B, Hkv, R, n, Lmax, W, nblk;
-    int block_units;            // stages per scale block
+    int block;                  // positions per scale block
+    int stage_log2, block_units;  // set at the launch: positions per stage, stages per scale block
     float scale_log2;
     unsigned long long timeout_ns;
 };

@@ -53,8 +53,7 @@
 // takes 2,650 to 3,000 cycles a stage, of which HBM alone asks 2,850; the kernel's end and
 // the combine take 4 us.  With several drafts the issue of a stage's 770 instructions
 // (530 for one token) is as long as its fetch.
-// Tried and left out: 64-position stages (more instructions a warp in a row: 16 drafts
-// batch 70 us), paired fp32 instructions for the state (register moves: 72 us), chunks of
+// Tried and left out: 64-position stages (the batch with drafts 70 us), paired fp32 instructions for the state (register moves: 72 us), chunks of
 // the list's end fetched by a counter (64 sequences 220 us), rows finished by the last CTA
 // of a pair instead of a second kernel (drafts 86 us), q fetched ahead (no change).
 #include <cuda_bf16.h>
@@ -77,7 +76,8 @@ constexpr int kWordsMax = 1024; // sequences whose length and gate decision a CT
 
 template <int D, int NT>
 struct D8 {
-    static constexpr int kTile = kDec8Stage * D;                  // codes of K (or V) of one stage, bytes
+    static constexpr int kStage = dec8_stage(D);                  // positions of a stage
+    static constexpr int kTile = kStage * D;                      // codes of K (or V) of one stage, bytes
     static constexpr int kStageBytes = 2 * kTile;                 // K then V
     static constexpr int kRingBytes = 16384;                      // of a warp; 128 KB in flight on an SM
     static constexpr int kStages = kRingBytes / kStageBytes;      // ring depth
@@ -91,7 +91,7 @@ struct D8 {
     static constexpr int kWarps = NT == 4 && D == 128 ? 6 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSmem = kWarps * kWarpBytes + 1024;      // + alignment slack
-    static constexpr int MT = kDec8Stage / 16;                    // 16-position tiles of a stage
+    static constexpr int MT = kStage / 16;                        // 16-position tiles of a stage
     static_assert(kStages >= 2 && kSmem + 6 * 1024 <= 227 * 1024 && kWarps * 148 <= kDec8MaxWarps, "launch shape");
 };
 
@@ -142,9 +142,10 @@ struct Plan {
         if (word == kBadLength) return;
         len = (int)(word & ~kGlobalBit);
         const int e0 = len - p.n - p.W + 1, e1 = len - p.W;  // window edges of the first and last token
-        in0 = e0 > 0 ? e0 / kDec8Stage : 0;
-        in1 = (len + kDec8Stage - 1) / kDec8Stage;
-        out = (word & kGlobalBit) && e1 > 0 ? (e1 + kDec8Stage - 1) / kDec8Stage : 0;
+        const int up = (1 << p.stage_log2) - 1;
+        in0 = e0 > 0 ? e0 >> p.stage_log2 : 0;
+        in1 = (len + up) >> p.stage_log2;
+        out = (word & kGlobalBit) && e1 > 0 ? (e1 + up) >> p.stage_log2 : 0;
     }
     __device__ __forceinline__ int stages() const { return out + in1 - in0; }
     __device__ __forceinline__ int units() const { return stages() + (len > 0 ? 1 : 0) + (out > 0 ? 1 : 0); }
@@ -187,6 +188,18 @@ struct Shares {
 // states and writes one for the run's first warp in the CTA.  A run that ends inside a
 // warp's share is written by that warp alone.
 //
+// Behind the workspace's header: for every sequence the units ahead of it, then the whole
+// list's (written by CTA 0, read by the combine kernel where the batch is large).
+__host__ __device__ inline long long prefix8(long long B) { return (B + 1 + 63) / 64 * 64; }
+__device__ __forceinline__ int* prefix_of(const Decode8Params& p)
+{
+    return reinterpret_cast<int*>(p.part) - prefix8(p.B);
+}
+// Sequences up to which a CTA of the combine kernel adds up the lengths itself, while the
+// partial kernel runs (10.0 us for short contexts, else 10.6); above that the sums of all its
+// CTAs took as long as the attention (512 short sequences: combine 57 us).
+constexpr int kScanMax = 64;
+
 // Partial states lie in slots of R rows and two kinds, (m, l) and o apart.  Slot (warp of
 // the grid + pair) is unique, since along the list either the warp or the pair moves on.
 __host__ __device__ inline long long slots8(long long pairs) { return kDec8MaxWarps + pairs; }
@@ -437,8 +450,8 @@ __device__ __forceinline__ void issue_unit(const Decode8Params& p, Ring8& ring, 
         // the warp's reads of this stage come before the copy engine's writes
         if (ring.issued >= (uint32_t)G::kStages) fence_proxy_async_smem();
         mbar_arrive_expect_tx(&ring.full[s], G::kStageBytes);
-        tma_load_3d(dst, &p.tm_k, &ring.full[s], 0, stage * kDec8Stage, pair, policy_evict_first());
-        tma_load_3d(dst + G::kTile, &p.tm_v, &ring.full[s], 0, stage * kDec8Stage, pair, policy_evict_first());
+        tma_load_3d(dst, &p.tm_k, &ring.full[s], 0, stage * G::kStage, pair, policy_evict_first());
+        tma_load_3d(dst + G::kTile, &p.tm_v, &ring.full[s], 0, stage * G::kStage, pair, policy_evict_first());
         units[s] = make_int4(2 * pair + (inside ? 0 : 1), stage, at.pl.len, 0);
     }
     ++ring.issued;
@@ -517,7 +530,7 @@ __device__ __noinline__ bool mask_values(uint32_t tileV, int pos0, int lo0, int 
     const int last = hi0 + n - 1;
     bool nan = false;
     #pragma unroll 1
-    for (int k = lane; k < kDec8Stage * D / 16; k += 32) {
+    for (int k = lane; k < dec8_stage(D) * D / 16; k += 32) {
         const int pos = pos0 + k / (D / 16);
         uint4* at = reinterpret_cast<uint4*>(v + 16 * k);
         if (pos < lo0 || pos > last) {
@@ -540,7 +553,7 @@ __device__ __forceinline__ void place_nan(uint32_t tileV, int pos0, int lo0, int
     const int lane = threadIdx.x & 31, g = lane >> 2;
     uint8_t* v = reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(tileV));
     #pragma unroll 1
-    for (int r = 0; r < kDec8Stage; ++r) {
+    for (int r = 0; r < dec8_stage(D); ++r) {
         const int pos = pos0 + r;
         if (pos < lo0 || pos > hi0 + n - 1 || (pos >= lo0 + n - 1 && pos <= hi0)) continue;  // seen by none or by all
         #pragma unroll
@@ -570,7 +583,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
 {
     using G = D8<D, NT>;
     constexpr int MT = G::MT;
-    static_assert(MT == 2, "a stage is one ldmatrix of V^T per 16 columns");
+    constexpr int H = MT / 2;  // ldmatrix of V^T per 16 columns: 32 positions each
     const int lane = threadIdx.x & 31, g = lane >> 2;
     const uint32_t tileV = tileK + G::kTile;
     if (masked && mask_values<TYPE, D>(tileV, pos0, lo0, hi0, n) && TYPE == kCacheE4M3)
@@ -592,10 +605,12 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
         #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             uint32_t w[4];
-            if (mt == 0)
-                ldsm4<0>(kat ^ (kk << 5), w);
-            else
-                ldsm4<16 * D>(kat ^ (kk << 5), w);
+            switch (mt) {
+                case 0: ldsm4<0>(kat ^ (kk << 5), w); break;
+                case 1: ldsm4<16 * D>(kat ^ (kk << 5), w); break;
+                case 2: ldsm4<32 * D>(kat ^ (kk << 5), w); break;
+                default: ldsm4<48 * D>(kat ^ (kk << 5), w); break;
+            }
             #pragma unroll
             for (int q = 0; q < 4; ++q) to_f16<TYPE>(w[q], x[mt][q], y[mt][q]);
             #pragma unroll
@@ -632,7 +647,9 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
                     for (int h = 0; h < 2; ++h)
                         if (16 * mt + 8 * h < lo || 16 * mt + 8 * h > hi) sc[mt][nt][2 * h + c] = -INFINITY;
             }
-            float mx = fmax3(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), sc[1][nt][c], sc[1][nt][2 + c]);
+            float mx = fmaxf(sc[0][nt][c], sc[0][nt][2 + c]);
+            #pragma unroll
+            for (int mt = 1; mt < MT; ++mt) mx = fmax3(mx, sc[mt][nt][c], sc[mt][nt][2 + c]);
             #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             const float mn = fmaxf(st.m[nt][c], fmaf(mx, f[c], -kPBias));
@@ -676,40 +693,42 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
         if (TYPE == kCacheInt8) {
             float ones[4];
             mma_f16_from(ones, kOnes, kOnes, kOnes, kOnes, pb[0][nt][0], pb[0][nt][1], 0.f, 0.f, 0.f, 0.f);
-            mma_f16(ones, kOnes, kOnes, kOnes, kOnes, pb[1][nt][0], pb[1][nt][1]);
+            #pragma unroll
+            for (int mt = 1; mt < MT; ++mt) mma_f16(ones, kOnes, kOnes, kOnes, kOnes, pb[mt][nt][0], pb[mt][nt][1]);
             o0[nt][0] = ones[0] * kInt8Shift;
             o0[nt][1] = ones[1] * kInt8Shift;
         }
     }
     vs *= kVScale<TYPE>;
     const uint32_t vat = swz<D>(tileV, lane, 0);
-    constexpr int UG = 2;  // column groups of 16 in flight
     #pragma unroll
-    for (int u0 = 0; u0 < D / 16; u0 += UG) {
-        uint32_t ev[UG][4], od[UG][4];
-        float acc[UG][NT][4];
+    for (int u = 0; u < D / 16; ++u) {
+        uint32_t ev[H][4], od[H][4];
         #pragma unroll
-        for (int j = 0; j < UG; ++j) {
+        for (int h = 0; h < H; ++h) {
             uint32_t w[4];
-            ldsm4t<0>(vat ^ ((u0 + j) << 4), w);
+            if (h == 0)
+                ldsm4t<0>(vat ^ (u << 4), w);
+            else
+                ldsm4t<32 * D>(vat ^ (u << 4), w);
             #pragma unroll
-            for (int i = 0; i < 4; ++i) to_f16_pairs<TYPE>(w[i], ev[j][i], od[j][i]);
-            #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma_f16_from(acc[j][nt], ev[j][0], od[j][0], ev[j][1], od[j][1], pb[0][nt][0], pb[0][nt][1], o0[nt][0],
-                             o0[nt][1], o0[nt][0], o0[nt][1]);
+            for (int i = 0; i < 4; ++i) to_f16_pairs<TYPE>(w[i], ev[h][i], od[h][i]);
         }
+        float acc[NT][4];
         #pragma unroll
-        for (int j = 0; j < UG; ++j)
+        for (int nt = 0; nt < NT; ++nt)
+            mma_f16_from(acc[nt], ev[0][0], od[0][0], ev[0][1], od[0][1], pb[0][nt][0], pb[0][nt][1], o0[nt][0], o0[nt][1],
+                         o0[nt][0], o0[nt][1]);
+        #pragma unroll
+        for (int mt = 1; mt < MT; ++mt)
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                mma_f16(acc[j][nt], ev[j][2], od[j][2], ev[j][3], od[j][3], pb[1][nt][0], pb[1][nt][1]);
+                mma_f16(acc[nt], ev[mt / 2][2 * (mt & 1)], od[mt / 2][2 * (mt & 1)], ev[mt / 2][2 * (mt & 1) + 1],
+                        od[mt / 2][2 * (mt & 1) + 1], pb[mt][nt][0], pb[mt][nt][1]);
         #pragma unroll
-        for (int j = 0; j < UG; ++j)
+        for (int nt = 0; nt < NT; ++nt)
             #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                #pragma unroll
-                for (int e = 0; e < 4; ++e) st.o[u0 + j][nt][e] = fmaf(acc[j][nt][e], vs, st.o[u0 + j][nt][e]);
+            for (int e = 0; e < 4; ++e) st.o[u][nt][e] = fmaf(acc[nt][e], vs, st.o[u][nt][e]);
     }
 }
 
@@ -747,8 +766,11 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
         bad |= w == kBadLength;
         mine = Plan(p, w);
         incl = warp_scan(mine.units()) * p.Hkv;
+        if (p.B > kScanMax && blockIdx.x == 0 && warp == G::kWarps - 1 && b < p.B)
+            prefix_of(p)[b] = T + incl - mine.units() * p.Hkv;
         T += __shfl_sync(0xffffffffu, incl, 31);
     }
+    if (p.B > kScanMax && blockIdx.x == 0 && threadIdx.x == 0) prefix_of(p)[p.B] = T;
     if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.status, kStatusBadArgument);
     const Shares ctas(T, (int)gridDim.x);
     const int cta = (int)blockIdx.x;
@@ -788,7 +810,7 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
     Ring8 ring{base, full_bars[warp], 0, 0};
     int run = -1, lo0 = 0, hi0 = 0, first = 0, last = 0;
     float ks32 = 0.f, vs32 = 0.f;  // scales of stages first .. first + 31, one per lane
-    bool ok = true;
+    bool ok = true, new_q = false;
     Rows8<NT> rw;
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -825,9 +847,8 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
             lo0 = inside ? unit.z - p.n - p.W + 1 : -kDec8MaxRows;
             hi0 = unit.z - p.n - (inside ? 0 : p.W);
             first = -64;
-            last = (unit.z - 1) / kDec8Stage;
-            const int pair = unit.x >> 1;
-            if (run < 0 || pair != run >> 1) stage_q<TYPE, D, NT>(p, pair, qs, rw);
+            last = (unit.z - 1) / G::kStage;
+            new_q = run < 0 || (unit.x ^ run) > 1;
             run = unit.x;
             st.init();
         }
@@ -837,13 +858,15 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
             ks32 = p.k_scale[(long long)(run >> 1) * p.nblk + blk];
             vs32 = p.v_scale[(long long)(run >> 1) * p.nblk + blk];
         }
+        if (new_q) stage_q<TYPE, D, NT>(p, run >> 1, qs, rw);  // while the scales are on their way
+        new_q = false;
         const float ks = __shfl_sync(0xffffffffu, ks32, unit.y - first), vs = __shfl_sync(0xffffffffu, vs32, unit.y - first);
         const uint32_t parity = (ring.used / G::kStages) & 1;
         ok = mbar_try_wait(&ring.full[s], parity) || wait_long(&ring.full[s], parity, abort_flag, p.status, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int pos0 = unit.y * kDec8Stage;
-        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + kDec8Stage - 1 > hi0;
+        const int pos0 = unit.y * G::kStage;
+        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + G::kStage - 1 > hi0;
         do_stage<TYPE, D, NT>(st, rw, qs, ring.base + s * G::kStageBytes, ks, vs, masked, pos0, lo0, hi0, p.n);
         ++ring.used;
         __syncwarp();  // every lane is done with the stage
@@ -889,7 +912,6 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
     constexpr int kWarps = D8<D, NT>::kWarps;
     __shared__ float red_m[2][kCombineWarps], red_l[2][kCombineWarps];
     __shared__ alignas(16) float red_o[2][kCombineWarps][D];
-    __shared__ uint32_t s_word;
     __shared__ int s_before[kCombineWarps], s_T[kCombineWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = (int)blockDim.x >> 5;
     const int pair = (int)(blockIdx.x / (unsigned)p.R), r = (int)(blockIdx.x % (unsigned)p.R);
@@ -897,26 +919,31 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
     const float gate = p.gate[(long long)b * p.n + tok];
     const bool sel = takes_global(gate, *p.tau);
     int T = 0, before = 0;
-    for (int i = tid; i < p.B; i += (int)blockDim.x) {
-        const uint32_t w = word_from(p, i);
-        const int un = Plan(p, w).units() * p.Hkv;
-        T += un;
-        if (i < b) before += un;
-        if (i == b) s_word = w;
+    if (p.B <= kScanMax) {
+        for (int i = tid; i < p.B; i += (int)blockDim.x) {
+            const int un = Plan(p, word_from(p, i)).units() * p.Hkv;
+            T += un;
+            if (i < b) before += un;
+        }
+        T = (int)__reduce_add_sync(0xffffffffu, T);
+        before = (int)__reduce_add_sync(0xffffffffu, before);
+        if (lane == 0) s_T[warp] = T, s_before[warp] = before;
+        __syncthreads();
+        T = before = 0;
+        for (int w = 0; w < nw; ++w) T += s_T[w], before += s_before[w];
     }
-    T = (int)__reduce_add_sync(0xffffffffu, T);
-    before = (int)__reduce_add_sync(0xffffffffu, before);
-    if (lane == 0) s_T[warp] = T, s_before[warp] = before;
-    __syncthreads();
-    T = before = 0;
-    for (int w = 0; w < nw; ++w) T += s_T[w], before += s_before[w];
-    const Plan pl(p, s_word);
+    const Plan pl(p, word_from(p, b));
     if (p.selected && hk == 0 && r < p.n && tid == 0) p.selected[(long long)b * p.n + r] = sel ? 1 : 0;
     uint16_t* out = p.out + ((long long)pair * p.R + r) * D;
     if (pl.len < p.n - tok) {  // the token lies before the sequence's start, or the length is invalid
         asm volatile("griddepcontrol.wait;" ::: "memory");  // no CTA ends ahead of the partial kernel
         for (int c = tid; c < D; c += (int)blockDim.x) out[c] = 0;
         return;
+    }
+    if (p.B > kScanMax) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        before = __ldcg(prefix_of(p) + b);
+        T = __ldcg(prefix_of(p) + p.B);
     }
     // Where the row's states lie: for each CTA that the run reaches into, the slot of the run's
     // first warp there; and the run's last warp's own where its share goes on behind the run.
@@ -1112,11 +1139,15 @@ cudaError_t launch_td(const Decode8Params& p, cudaStream_t stream)
 
 size_t decode8_partials_bytes(int B, int Hkv, int R, int d)
 {
-    return (size_t)slots8((long long)B * Hkv) * 2 * R * (d + 2) * sizeof(float);
+    return (size_t)(prefix8(B) + slots8((long long)B * Hkv) * 2 * R * (d + 2)) * sizeof(float);
 }
 
-cudaError_t launch_decode8(const Decode8Params& p, int type, int d, cudaStream_t stream)
+cudaError_t launch_decode8(const Decode8Params& params, int type, int d, cudaStream_t stream)
 {
+    Decode8Params p = params;
+    p.part += prefix8(p.B);
+    p.stage_log2 = d == 64 ? 6 : 5;
+    p.block_units = p.block >> p.stage_log2;
     if (type == kCacheE4M3) return d == 64 ? launch_td<kCacheE4M3, 64>(p, stream) : launch_td<kCacheE4M3, 128>(p, stream);
     return d == 64 ? launch_td<kCacheInt8, 64>(p, stream) : launch_td<kCacheInt8, 128>(p, stream);
 }
