@@ -334,3 +334,67 @@ def test_a_serving_loop(dtype):
         for b in range(B):
             for x in "kv":
                 model.rows[x][b] = model.rows[x][b][:, :lens[b]]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scores_far_below_zero_and_rising(dtype):
+    """Scores around -1e31 are a softmax like any other; and scores that rise from stage to stage by a little more or
+    less than what a stage may exceed the ones before it."""
+    B, d, L = 1, 64, 640
+    gen = torch.Generator().manual_seed(17)
+    cache, model = fresh(B, 1, L, d, dtype, 64), ref.Model(B, 1, d, dtype, 64)
+    k = torch.zeros(1, 1, L, d)
+    k[..., 0] = -1.0
+    v = torch.randn(1, 1, L, d, generator=gen)
+    fill(cache, model, k.bfloat16(), v.bfloat16(), [0, L], [L])
+    q = torch.zeros(1, 2, 1, d)
+    q[0, 0, 0, 0], q[0, 1, 0, 0] = 8e31, -8e31
+    gate = torch.tensor([[1.0]])
+    ws = logo.decode8_workspace(cache, 2)
+    for tau in (0.0, 2.0):
+        out, sel = logo.decode8(q.bfloat16().cuda(), cache, ints([L]), gate.cuda(), torch.tensor([tau], device="cuda"), 100,
+                                ws=ws)
+        logo.check(ws)
+        # every score is the same, so the weights are: the mean of the values
+        vals = model.values("v", 0)
+        want = vals[:, -100:].mean(1) + (torch.sigmoid(torch.tensor(1.0)).item() * vals.mean(1) if tau < 1 else 0)
+        assert (out[0, :, 0].double().cpu() - want).abs().max().item() <= 2.0 ** -8 * want.abs().max().item() + 2.0 ** -9
+    for step in (0.5, 1.2, 1.4, 3.0):
+        cache, model = fresh(B, 1, L, d, dtype, 64), ref.Model(B, 1, d, dtype, 64)
+        k = torch.randn(1, 1, L, d, generator=gen) * 0.05
+        k[0, 0, :, 0] += torch.arange(L) // 32 * step       # 8 q.k / 8 rises by `step` (log2: 1.44 step) every 32 positions
+        fill(cache, model, k.bfloat16(), v.bfloat16(), [0, L], [L])
+        q = torch.zeros(1, 2, 1, d)
+        q[..., 0] = 8.0
+        q[0, 1] *= -1
+        go_gate = torch.tensor([[1.0]])
+        out, sel = logo.decode8(q.bfloat16().cuda(), cache, ints([L]), go_gate.cuda(), torch.tensor([0.0], device="cuda"), 300,
+                                ws=ws)
+        logo.check(ws)
+        verify(cache, model, q.bfloat16(), go_gate, 0.0, 300, [L], out, sel)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_equal_scores_of_any_size(dtype):
+    """Equal scores get equal weights where fp32 has no digits left behind the point: at 2^20 to 2^32 the reference
+    that is taken off the scores is itself rounded by up to 2^8."""
+    B, d, L, W = 1, 64, 640, 100
+    gen = torch.Generator().manual_seed(23)
+    cache, model = fresh(B, 1, L, d, dtype, 64), ref.Model(B, 1, d, dtype, 64)
+    k = torch.zeros(1, 1, L, d)
+    k[..., 0] = -1.0
+    v = torch.randn(1, 1, L, d, generator=gen)
+    fill(cache, model, k.bfloat16(), v.bfloat16(), [0, L], [L])
+    ws = logo.decode8_workspace(cache, 2)
+    vals = model.values("v", 0)
+    want = vals[:, -W:].mean(1)
+    # out is off by half a step of bf16 (2^-8 of it), and each P by 2^-11 of itself against the sum of unrounded P
+    tol = 2.0 ** -8 * want.abs() + 1.01 * 2.0 ** -11 * vals[:, -W:].abs().mean(1) + 1e-5
+    for e in range(20, 33):
+        for x in (1.0, 1.375, 1.9375):
+            q = torch.zeros(1, 2, 1, d)
+            q[0, 0, 0, 0], q[0, 1, 0, 0] = 8 * x * 2.0 ** e, -8 * x * 2.0 ** e
+            out, sel = logo.decode8(q.bfloat16().cuda(), cache, ints([L]), torch.ones(1, 1).cuda(),
+                                    torch.tensor([2.0], device="cuda"), W, ws=ws)
+            logo.check(ws)
+            assert ((out[0, :, 0].double().cpu() - want).abs() <= tol).all(), (e, x)

@@ -11,8 +11,8 @@
 // Bound by HBM: one byte per element of the cache read, about 2 R FLOP per byte for
 // the R = (Hq / Hkv) n query rows that share a key/value head.
 //   decode8_partial_kernel  one wave of persistent warps, 8 to an SM.  The work is a
-//     list of units: for every (sequence, key/value head) the 32-position stages before
-//     the window (only where a token is global), then the stages that reach into it.
+//     list of units: for every (sequence, key/value head) the stages (8 KB of K and V: 32
+//     positions, 64 at d = 64) before the window (only where a token is global), then the stages that reach into it.
 //     The list is cut into equal shares, one per warp, so every warp reads about the
 //     same number of bytes whatever the lengths and gates are; the lengths are read on
 //     the device.  A warp streams its stages through a private ring of 16 KB in shared
@@ -23,7 +23,7 @@
 //                     order of the head dimension inside a product is free, so a lane
 //                     uses the four consecutive codes that ldmatrix gives it as they
 //                     are, and q is stored in that order.
-//       softmax       online, fp32, one maximum per stage and query row;
+//       softmax       online, fp32; a maximum is taken only in stages that need one;
 //       O^T += V^T P^T  V^T by ldmatrix.trans on pairs of codes: a word holds two
 //                     head-dimension columns at two positions, and one byte permute
 //                     sorts it into the fp16 pairs of two rows of V^T.  Each stage's
@@ -42,20 +42,23 @@
 //
 // Roundings: q is scaled by a power of two per row, so that its largest element lies
 // in [2^14, 2^15), and rounded to fp16 (exact for elements down to 2^-28 of the
-// largest).  P is 2^15 exp2(s - m) in fp16: 11 bits, 3 more than bf16, with values
-// down to 2^-39 of the largest kept.  The sum l uses the unrounded P.
+// largest).  P is held near 2^14 times itself in fp16: 11 bits, 3 more than bf16, with
+// values down to 2^-38 of the largest kept.  The sum l uses the unrounded P.
 //
 // Measured (d = 128, 32 query heads on 8, e4m3, window 4096; bytes that have to be read
-// over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 214 us (0.92);
-// one global sequence of 128K beside a local one 50 us (0.84); one of 32K 19.6 us (0.52);
-// 16 of 8K to 32K with four drafted tokens each 63 us (0.64); two of 4K 9.5 us.  Once its
+// over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 215 us (0.92);
+// one global sequence of 128K beside a local one 50.5 us (0.84); one of 32K 19.3 us (0.53);
+// 16 of 8K to 32K with four drafted tokens each 58.8 us (0.68); two of 4K 9.2 us.  Once its
 // first bytes are there (5 us: launch, lengths, the first 19 MB of all SMs' rings), a warp
 // takes 2,650 to 3,000 cycles a stage, of which HBM alone asks 2,850; the kernel's end and
-// the combine take 4 us.  With several drafts the issue of a stage's 770 instructions
-// (530 for one token) is as long as its fetch.
-// Tried and left out: 64-position stages (the batch with drafts 70 us), paired fp32 instructions for the state (register moves: 72 us), chunks of
-// the list's end fetched by a counter (64 sequences 220 us), rows finished by the last CTA
-// of a pair instead of a second kernel (drafts 86 us), q fetched ahead (no change).
+// the combine take 4 us.  With 16 rows and more the issue of a stage's instructions is as
+// long as its fetch (370 MB for 4, 16 and 32 rows a key/value head: 62, 75 and 122 us).
+// A maximum for every stage in place of kPMargin: four drafts 64.6 us, 32 rows 185 us (with
+// the six warps that its registers allowed), one token the same.
+// Tried and left out: 64-position stages at d = 128 (four drafts 70 us), paired fp32
+// instructions for the state (register moves: 72 us), chunks of the list's end fetched by a
+// counter (64 sequences 220 us), rows finished by the last CTA of a pair instead of a second
+// kernel (drafts 86 us), q fetched ahead (no change).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -71,7 +74,14 @@ namespace logo {
 
 namespace {
 
-constexpr float kPBias = 15.f;  // P is held times 2^15: the state's m is the maximum less 15
+// P is held as 2^(s + nr): nr is kPBias less a maximum that the scores seen so far exceed by
+// at most kPMargin, so that P stays below 2^16 and in fp16, and nearly every stage is done
+// without finding its maximum across lanes or touching O.
+// Scores are rounded to fp32 before nr is added, and nr is rounded down: however large they
+// are, equal scores get equal P, and none above 2^(kPBias + kPMargin).  (The product in one
+// multiply-add with nr would keep digits of it that nr has lost: infinite P at scores of 1e31.)
+constexpr float kPBias = 14.f, kPMargin = 1.9f;
+constexpr float kEmpty = 3.402823466e38f;  // nr while nothing was seen: scores above -kEmpty exceed it
 constexpr int kWordsMax = 1024; // sequences whose length and gate decision a CTA keeps in shared memory
 
 template <int D, int NT>
@@ -85,10 +95,10 @@ struct D8 {
     static constexpr int kStateBytes = 8 * NT * (D + 2) * 4;      // partial state, written over the ring at the end
     static constexpr int kUsedBytes = kRingBytes + kQBytes > kStateBytes ? kRingBytes + kQBytes : kStateBytes;
     static constexpr int kWarpBytes = (kUsedBytes + 1023) / 1024 * 1024;
-    // Two warps on every scheduler, and registers and shared memory left for the combine
-    // kernel's CTAs (12 warps: they wait for the others to end, 10.4 -> 13.9 us for short
-    // contexts, 21.0 -> 25.0 us for one of 32K); six where 32 rows of O fill the registers.
-    static constexpr int kWarps = NT == 4 && D == 128 ? 6 : 8;
+    // Two warps on every scheduler, and (up to 16 rows) registers and shared memory left for
+    // the combine kernel's CTAs (12 warps: they wait for the others to end, 10.4 -> 13.9 us for
+    // short contexts, 21.0 -> 25.0 us for one of 32K).
+    static constexpr int kWarps = 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSmem = kWarps * kWarpBytes + 1024;      // + alignment slack
     static constexpr int MT = kStage / 16;                        // 16-position tiles of a stage
@@ -333,17 +343,17 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
 }
 
 // Softmax state of the warp's query rows.  Lane (g, t) = (lane / 4, lane % 4) has
-// columns 8 nt + 2t + c (c = 0, 1): their maxima (shared by the 8 lanes of the same
-// t), a share of their sums, and of O^T the rows 16 u + 2g + h at o[u][nt][2h + c].
+// columns 8 nt + 2t + c (c = 0, 1): their nr (shared by the 8 lanes of the same t; the
+// state that is written has m = -nr), a share of their sums, and of O^T the rows
+// 16 u + 2g + h at o[u][nt][2h + c].
 template <int D, int NT>
 struct State8 {
-    float m[NT][2];
-    float l[NT][2];
+    float nr[NT][2], l[NT][2];
     float o[D / 16][NT][4];
     __device__ __forceinline__ void init()
     {
         #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) nr[nt][0] = nr[nt][1] = kEmpty, l[nt][0] = l[nt][1] = 0.f;
         #pragma unroll
         for (int u = 0; u < D / 16; ++u)
             #pragma unroll
@@ -376,7 +386,7 @@ __device__ __forceinline__ void store_state8(State8<D, NT>& st, int R, float2* m
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int r = 8 * nt + 2 * t + c;
-            store_if(r < R && g == 0, ml + r, st.m[nt][c], st.l[nt][c] * kLScale<TYPE>);
+            store_if(r < R && g == 0, ml + r, -st.nr[nt][c], st.l[nt][c] * kLScale<TYPE>);
             float* row = o + r * D + 2 * g;
             #pragma unroll
             for (int u = 0; u < D / 16; ++u)
@@ -628,17 +638,19 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
             for (int nt = 0; nt < NT; ++nt)
                 mma_f16(sc[mt][nt], x[mt][2], x[mt][3], y[mt][2], y[mt][3], b1[nt].x, b1[nt].y);
     }
-    // Online softmax.  The maximum is taken over the products before their (positive) factor,
-    // which meets them in the exponent's multiply-add.
+    // Online softmax, in units of log2.
     uint32_t pb[MT][NT][2];
-    float al[NT][2];
+    float mx[NT][2];
+    bool over = false;
     #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float f[2], nr[2];
+    for (int nt = 0; nt < NT; ++nt)
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            f[c] = ks * rw.qf[nt][c];
-            f[c] = f[c] < 1.17549435e-38f ? 1.17549435e-38f : f[c];  // so that it leaves -inf as it is
+            const float f = ks * rw.qf[nt][c];
+            #pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) sc[mt][nt][2 * h + c] = __fmul_rn(sc[mt][nt][2 * h + c], f);
             if (masked) {
                 const int lo = lo0 + rw.tok[nt][c] - pos0 - g, hi = hi0 + rw.tok[nt][c] - pos0 - g;
                 #pragma unroll
@@ -647,17 +659,33 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
                     for (int h = 0; h < 2; ++h)
                         if (16 * mt + 8 * h < lo || 16 * mt + 8 * h > hi) sc[mt][nt][2 * h + c] = -INFINITY;
             }
-            float mx = fmaxf(sc[0][nt][c], sc[0][nt][2 + c]);
+            mx[nt][c] = fmaxf(sc[0][nt][c], sc[0][nt][2 + c]);
             #pragma unroll
-            for (int mt = 1; mt < MT; ++mt) mx = fmax3(mx, sc[mt][nt][c], sc[mt][nt][2 + c]);
-            #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(st.m[nt][c], fmaf(mx, f[c], -kPBias));
-            nr[c] = mn == -INFINITY ? 0.f : -mn;
-            al[nt][c] = fast_exp2(st.m[nt][c] + nr[c]);  // 0 while nothing was seen
-            st.m[nt][c] = mn;
+            for (int mt = 1; mt < MT; ++mt) mx[nt][c] = fmax3(mx[nt][c], sc[mt][nt][c], sc[mt][nt][2 + c]);
+            over |= __fadd_rn(mx[nt][c], st.nr[nt][c]) > kPBias + kPMargin;
         }
-        float sum[2] = {0.f, 0.f};
+    if (__any_sync(0xffffffffu, over)) {
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float al[2];
+            #pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                #pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], off));
+                const float nr = fminf(st.nr[nt][c], __fsub_rd(kPBias, mx[nt][c]));
+                al[c] = fast_exp2(nr - st.nr[nt][c]);  // 0 while nothing was seen
+                st.nr[nt][c] = nr;
+                st.l[nt][c] *= al[c];
+            }
+            #pragma unroll
+            for (int u = 0; u < D / 16; ++u)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) st.o[u][nt][e] *= al[e & 1];
+        }
+    }
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
         #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             #pragma unroll
@@ -665,27 +693,13 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
                 float x[2];
                 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    x[c] = fast_exp2(fmaf(sc[mt][nt][2 * h + c], f[c], nr[c]));
-                    sum[c] += x[c];
+                    x[c] = fast_exp2(__fadd_rn(sc[mt][nt][2 * h + c], st.nr[nt][c]));
+                    st.l[nt][c] += x[c];
                 }
                 // P^T fragment: the score fragment's 8x8 quarter transposed in registers
                 pb[mt][nt][h] = movm(pack_f16x2(x[0], x[1]));
             }
-        #pragma unroll
-        for (int c = 0; c < 2; ++c) st.l[nt][c] = fmaf(st.l[nt][c], al[nt][c], sum[c]);
-    }
-    // O^T = O^T alpha + (V^T P^T) vs; most stages leave every maximum as it is
-    bool moved = false;
-    #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) moved |= al[nt][0] != 1.f || al[nt][1] != 1.f;
-    if (__any_sync(0xffffffffu, moved)) {
-        #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            #pragma unroll
-            for (int u = 0; u < D / 16; ++u)
-                #pragma unroll
-                for (int e = 0; e < 4; ++e) st.o[u][nt][e] *= al[nt][e & 1];
-    }
+    // O^T += (V^T P^T) vs
     float o0[NT][2];  // what the products start at: zero, or (int8) -128 2^-24 sum P
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
