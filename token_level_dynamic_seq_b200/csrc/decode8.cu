@@ -12,7 +12,8 @@
 // the R = (Hq / Hkv) n query rows that share a key/value head.
 //   decode8_partial_kernel  one wave of persistent warps, 8 to an SM.  The work is a
 //     list of units: for every (sequence, key/value head) the stages (8 KB of K and V: 32
-//     positions, 64 at d = 64) before the window (only where a token is global), then the stages that reach into it.
+//     positions, 64 at d = 64) before the window (only where a token is global), then the
+//     stages that reach into it.
 //     The list is cut into equal shares, one per warp, so every warp reads about the
 //     same number of bytes whatever the lengths and gates are; the lengths are read on
 //     the device.  A warp streams its stages through a private ring of 16 KB in shared
