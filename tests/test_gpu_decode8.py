@@ -398,3 +398,25 @@ def test_equal_scores_of_any_size(dtype):
                                     torch.tensor([2.0], device="cuda"), W, ws=ws)
             logo.check(ws)
             assert ((out[0, :, 0].double().cpu() - want).abs() <= tol).all(), (e, x)
+
+
+@pytest.mark.parametrize("B", [3, 70])
+def test_a_workspace_with_an_earlier_timeout(B):
+    """The status word of an earlier call whose wait ran out is reported again, whatever else the workspace holds; set
+    up anew, the workspace serves."""
+    lens = [(i * 29) % 200 for i in range(B)]
+    cache, model, gen = build(B, 2, 256, 128, TYPES[0], 64, lens, seed=29)
+    q, gate = torch.randn(B, 4, 1, 128, generator=gen).bfloat16(), torch.randn(B, 1, generator=gen)
+    tau = torch.zeros(1, device="cuda")
+    ws = logo.decode8_workspace(cache, 4)
+    ws.fill_(0x7f)
+    ws[:256] = 0
+    ws[0] = 1
+    logo.decode8(q.cuda(), cache, ints(lens), gate.cuda(), tau, 50, ws=ws)
+    with pytest.raises(logo.LogoError) as e:
+        logo.check(ws)
+    assert e.value.status == 5
+    ws[:256] = 0
+    out, sel = logo.decode8(q.cuda(), cache, ints(lens), gate.cuda(), tau, 50, ws=ws)
+    logo.check(ws)
+    verify(cache, model, q, gate, 0.0, 50, lens, out, sel)

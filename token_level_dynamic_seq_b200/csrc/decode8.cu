@@ -771,7 +771,6 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
     if (threadIdx.x == 0) abort_word = (was & kStatusTimeout) ? 1 : 0;
     __syncthreads();
     volatile int* abort_flag = &abort_word;
-    if (*abort_flag) return;
     // The whole list's length (every warp for itself).
     int T = 0, incl = 0;
     bool bad = false;
@@ -786,6 +785,9 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
         T += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (p.B > kScanMax && blockIdx.x == 0 && threadIdx.x == 0) prefix_of(p)[p.B] = T;
+    // An earlier call's wait ran out: nothing is attended to, but the combine kernel, which
+    // places its reads by them, has this call's sums.
+    if (*abort_flag) return;
     if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.status, kStatusBadArgument);
     const Shares ctas(T, (int)gridDim.x);
     const int cta = (int)blockIdx.x;
