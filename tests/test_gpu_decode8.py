@@ -420,3 +420,26 @@ def test_a_workspace_with_an_earlier_timeout(B):
     out, sel = logo.decode8(q.cuda(), cache, ints(lens), gate.cuda(), tau, 50, ws=ws)
     logo.check(ws)
     verify(cache, model, q, gate, 0.0, 50, lens, out, sel)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_the_largest_queries_and_values(dtype):
+    """Queries near bf16's largest against the smallest keys a scale stands for: one key is 1e6 ahead of the others,
+    so the output is its value, here up to 3e38.  Also a window beyond 32 bits: the whole cache."""
+    B, d, L, at = 1, 64, 200, 77
+    gen = torch.Generator().manual_seed(31)
+    cache, model = fresh(B, 1, L, d, dtype, 64), ref.Model(B, 1, d, dtype, 64)
+    k = torch.full((1, 1, L, d), -2.0 ** -100)
+    k[0, 0, at] = 2.0 ** -100
+    v = (torch.rand(1, 1, L, d, generator=gen) * 2 - 1).mul(3e38)
+    fill(cache, model, k.bfloat16(), v.bfloat16(), [0, L], [L])
+    q = torch.zeros(1, 2, 1, d)
+    q[0, :, 0, 5] = 3e38
+    ws = logo.decode8_workspace(cache, 2)
+    for W in (L, 2 ** 40):
+        out, sel = logo.decode8(q.bfloat16().cuda(), cache, ints([L]), torch.ones(1, 1).cuda(),
+                                torch.tensor([2.0], device="cuda"), W, ws=ws)
+        logo.check(ws)
+        want = model.values("v", 0)[:, at]
+        # the weight is one: half a step of bf16, and a few of fp32
+        assert ((out[0, :, 0].double().cpu() - want).abs() <= (2.0 ** -8 + 2.0 ** -20) * want.abs()).all()

@@ -281,12 +281,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 // Codes as fp16 pairs, exact.  e4m3: the code's value.  int8: (code + 128) 2^-24, a subnormal number whose bits are the code's with the sign bit turned; the
 // products' accumulators start at -128 2^-24 times the other operand's sum instead of zero.
 constexpr uint32_t kOnes = 0x3c003c00u;  // two fp16 ones
-// P's 2^15 and the codes' 2^-24 would take O out of range for values beyond 1e34: O is kept
+// P's 2^16 and the codes' 2^-24 would take O out of range for values beyond 1e34: O is kept
 // without them, and the state's l is given the same factor when it is written.
 template <int TYPE>
-constexpr float kVScale = TYPE == kCacheE4M3 ? 1.f / 32768.f : 1.f;
+constexpr float kVScale = TYPE == kCacheE4M3 ? 1.f / 131072.f : 1.f;
 template <int TYPE>
-constexpr float kLScale = TYPE == kCacheE4M3 ? 1.f / 32768.f : 1.f / 16777216.f;
+constexpr float kLScale = TYPE == kCacheE4M3 ? 1.f / 131072.f : 1.f / 16777216.f;
 constexpr float kInt8Unit = 16777216.f, kInt8Shift = -128.f / 16777216.f;
 
 template <int TYPE>
@@ -472,7 +472,8 @@ __device__ __forceinline__ void issue_unit(const Decode8Params& p, Ring8& ring, 
 // Per-lane constants of the (sequence, key/value head) at hand.
 template <int NT>
 struct Rows8 {
-    float qf[NT][2];  // scale * log2(e) / (the power of two in the row's fp16 q)
+    float qf[NT][2];  // scale * log2(e) / (the power of two in the row's fp16 q); int8's 2^24 apart: together
+                      // they pass 2^127 for q from 1e36 on, where the key's scale brings them back
     float s0[NT][2];  // what the scores' accumulators start at (int8)
     int tok[NT][2];   // the column's token
 };
@@ -522,7 +523,7 @@ __device__ __forceinline__ void stage_q(const Decode8Params& p, long long pair, 
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int e2 = __shfl_sync(0xffffffffu, ex, 4 * (2 * t + c));
-            rw.qf[nt][c] = p.scale_log2 * (TYPE == kCacheInt8 ? kInt8Unit : 1.f) * __uint_as_float((uint32_t)(127 - e2) << 23);
+            rw.qf[nt][c] = p.scale_log2 * __uint_as_float((uint32_t)(127 - e2) << 23);
             rw.s0[nt][c] = TYPE == kCacheInt8 ? kInt8Shift * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + c)) : 0.f;
         }
     }
@@ -647,7 +648,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
     for (int nt = 0; nt < NT; ++nt)
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const float f = ks * rw.qf[nt][c];
+            const float f = ks * rw.qf[nt][c] * (TYPE == kCacheInt8 ? kInt8Unit : 1.f);
             #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
                 #pragma unroll

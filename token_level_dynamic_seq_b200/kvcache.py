@@ -203,7 +203,7 @@ def decode8(q, cache: Cache8, cache_len, gate, tau, window: int, ws=None, scale:
         _used_on(stream, selected)
     _logo._raise(lib.logo_decode8(
         _at(cache, q, torch.bfloat16, 0, "q"), cache._ref, _at(cache, cache_len, torch.int32, B, "cache_len"),
-        _at(cache, gate, torch.float32, B * n, "gate"), _at(cache, tau, torch.float32, 1, "tau"), Hq, n, int(window),
+        _at(cache, gate, torch.float32, B * n, "gate"), _at(cache, tau, torch.float32, 1, "tau"), Hq, n, min(int(window), 0x7fffffff),
         float(scale), _at(cache, out, torch.bfloat16, 0, "out"), _at(cache, selected, torch.int32, B * n, "selected"),
         _at(cache, ws, torch.uint8, 0, "ws"), ws.numel(), _queue(cache, stream)))
     return out, selected
