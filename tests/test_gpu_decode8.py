@@ -443,3 +443,24 @@ def test_the_largest_queries_and_values(dtype):
         want = model.values("v", 0)[:, at]
         # the weight is one: half a step of bf16, and a few of fp32
         assert ((out[0, :, 0].double().cpu() - want).abs() <= (2.0 ** -8 + 2.0 ** -20) * want.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_offsets_beyond_32_bits(dtype):
+    """Rows at positions around 2^26 of two heads with 64 codes each: 2^32 bytes into either slab and 2^33 in all."""
+    s, L, W, d, Hkv = 2 ** 26 - 64, 300, 200, 64, 2
+    gen = torch.Generator().manual_seed(37)
+    cache, model = logo.cache8(1, Hkv, s + 400, d, "cuda", dtype=dtype, block=64), ref.Model(1, Hkv, d, dtype, 64)
+    k, v = (torch.randn(1, Hkv, L, d, generator=gen).bfloat16() for _ in "kv")
+    ws = logo.decode8_workspace(cache, 4, 2)
+    held = torch.zeros(1, dtype=torch.int32, device="cuda")
+    logo.cache8_append(cache, k.cuda(), v.cuda(), ints([s]), ws=ws, new_len=held)
+    assert held.item() == s + L
+    model.append(0, 0, k[0], v[0])
+    q, gate = torch.randn(1, 4, 2, d, generator=gen).bfloat16(), torch.full((1, 2), -1.0)
+    out, sel = logo.decode8(q.cuda(), cache, held, gate.cuda(), torch.zeros(1, device="cuda"), W, ws=ws)
+    kb, vb = logo.cache8_read(cache, ints([s]), L, ws=ws)
+    logo.check(ws)
+    verify(cache, model, q, gate, 0.0, W, [L], out, sel)
+    for x, got in (("k", kb), ("v", vb)):
+        assert torch.equal(got[0].cpu(), model.values(x, 0).float().bfloat16())

@@ -47,7 +47,8 @@
 // values down to 2^-38 of the largest kept.  The sum l uses the unrounded P.
 //
 // Measured (d = 128, 32 query heads on 8, e4m3, window 4096; bytes that have to be read
-// over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 215 us (0.92);
+// over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 219 us
+// (0.91; 195 to 215 where a call finds what the one before left in L2);
 // one global sequence of 128K beside a local one 50.5 us (0.84); one of 32K 19.3 us (0.53);
 // 16 of 8K to 32K with four drafted tokens each 58.8 us (0.68); two of 4K 9.2 us.  Once its
 // first bytes are there (5 us: launch, lengths, the first 19 MB of all SMs' rings), a warp
