@@ -54,7 +54,7 @@
 // first bytes are there (5 us: launch, lengths, the first 19 MB of all SMs' rings), a warp
 // takes 2,650 to 3,000 cycles a stage, of which HBM alone asks 2,850; the kernel's end and
 // the combine take 4 us.  With 16 rows and more the issue of a stage's instructions is as
-// long as its fetch (370 MB for 4, 16 and 32 rows a key/value head: 62, 75 and 122 us).
+// long as its fetch (370 MB for 4, 16, 24 and 32 rows a key/value head: 62, 74, 100, 122 us).
 // A maximum for every stage in place of kPMargin: four drafts 64.6 us, 32 rows 185 us (with
 // the six warps that its registers allowed), one token the same.
 // Tried and left out: 64-position stages at d = 128 (four drafts 70 us), paired fp32
@@ -1147,11 +1147,15 @@ cudaError_t launch_tdn(const Decode8Params& p, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, decode8_combine_kernel<D, NT>, p, grid);
 }
 
+// Products, exponentials and O's registers go by eights of rows, so each count of eights has
+// its kernel (24 rows in that of 32, 371 MB: e4m3 119 against 100 us, int8 132 against 105;
+// d = 64, 186 MB: 74 against 58, 76 against 63).
 template <int TYPE, int D>
 cudaError_t launch_td(const Decode8Params& p, cudaStream_t stream)
 {
     return p.R <= 8 ? launch_tdn<TYPE, D, 1>(p, stream)
-                    : p.R <= 16 ? launch_tdn<TYPE, D, 2>(p, stream) : launch_tdn<TYPE, D, 4>(p, stream);
+           : p.R <= 16 ? launch_tdn<TYPE, D, 2>(p, stream)
+           : p.R <= 24 ? launch_tdn<TYPE, D, 3>(p, stream) : launch_tdn<TYPE, D, 4>(p, stream);
 }
 
 }  // namespace
