@@ -132,19 +132,19 @@ __device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32_t w1, float inv)
 }
 
 // The rows that sequence b brings and where they lie in its head slab.  False (and
-// reported) when the offsets or the target range are out of range.
+// reported) when the offsets or the target range are out of range; s is set all the same.
 __device__ __forceinline__ bool span_of(const int32_t* cu, const int32_t* start, int b, int n_slab, int max_n,
                                         int Lmax, int& row0, int& n, int& s)
 {
     row0 = 0;
     n = n_slab;
+    s = start[b];
     if (cu) {
         row0 = cu[b];
         const long long e = cu[b + 1];
         if (row0 < 0 || e < row0 || e > n_slab || e - row0 > max_n) return false;
         n = (int)(e - row0);
     }
-    s = start[b];
     return s >= 0 && (long long)s + n <= Lmax;
 }
 
