@@ -111,7 +111,8 @@ LOGO_API logo_status logo_cache8_read(const logo_cache8 *cache, const int32_t *s
  * be set up once with logo_workspace_init, and be used by one stream (or one
  * captured graph) at a time.
  * A key, value or scale that is not finite reaches the tokens that attend to its
- * position and no others.
+ * position (a scale's: its block) and no others; a value's scale that is not
+ * finite makes their outputs NaN.
  */
 LOGO_API size_t logo_decode8_workspace_size(const logo_cache8 *cache, int Hq, int n);
 LOGO_API logo_status logo_decode8(const logo_bf16 *q, const logo_cache8 *cache, const int32_t *cache_len,

@@ -83,8 +83,11 @@ namespace {
 // are, equal scores get equal P, and none above 2^(kPBias + kPMargin).  (The product in one
 // multiply-add with nr would keep digits of it that nr has lost: infinite P at scores of 1e31.)
 constexpr float kPBias = 14.f, kPMargin = 1.9f;
-constexpr float kEmpty = 3.402823466e38f;  // nr while nothing was seen: scores above -kEmpty exceed it
+constexpr float kLargest = 3.402823466e38f;
+constexpr float kEmpty = kLargest;  // nr while nothing was seen: scores above -kEmpty exceed it
 constexpr int kWordsMax = 1024; // sequences whose length and gate decision a CTA keeps in shared memory
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= kLargest; }
 
 template <int D, int NT>
 struct D8 {
@@ -589,7 +592,8 @@ __device__ __forceinline__ void place_nan(uint32_t tileV, int pos0, int lo0, int
     __syncwarp();
 }
 
-// One stage: scores, softmax step, products.  `masked`: some column sees it in part.
+// One stage: scores, softmax step, products.  `masked`: some column sees it in part, or the
+// V scale is not finite.
 template <int TYPE, int D, int NT>
 __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw, const uint2* qs, uint32_t tileK,
                                          float ks, float vs, bool masked, int pos0, int lo0, int hi0, int n)
@@ -599,8 +603,21 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
     constexpr int H = MT / 2;  // ldmatrix of V^T per 16 columns: 32 positions each
     const int lane = threadIdx.x & 31, g = lane >> 2;
     const uint32_t tileV = tileK + G::kTile;
-    if (masked && mask_values<TYPE, D>(tileV, pos0, lo0, hi0, n) && TYPE == kCacheE4M3)
-        place_nan<D, NT>(tileV, pos0, lo0, hi0, n, rw, st);
+    if (masked) {
+        if (mask_values<TYPE, D>(tileV, pos0, lo0, hi0, n) && TYPE == kCacheE4M3)
+            place_nan<D, NT>(tileV, pos0, lo0, hi0, n, rw, st);
+        if (!finite(vs)) {
+            // NaN for the columns that see the stage; the others' products are zero, which times
+            // such a scale would be NaN too.
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                #pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (lo0 + rw.tok[nt][c] < pos0 + G::kStage && hi0 + rw.tok[nt][c] >= pos0)
+                        st.l[nt][c] = __int_as_float(0x7fffffff);
+            vs = 0.f;
+        }
+    }
     // S^T = K q^T: rows = positions 16 mt + g (+ 8), columns = query rows.  ldmatrix: lane's row
     // lane mod 16 of the 16, 16-byte unit 2 kk + lane / 16; the swizzle turns into an exclusive or.
     float sc[MT][NT][4];
@@ -885,7 +902,7 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int pos0 = unit.y * G::kStage;
-        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + G::kStage - 1 > hi0;
+        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + G::kStage - 1 > hi0 || !finite(vs);
         do_stage<TYPE, D, NT>(st, rw, qs, ring.base + s * G::kStageBytes, ks, vs, masked, pos0, lo0, hi0, p.n);
         ++ring.used;
         __syncwarp();  // every lane is done with the stage
