@@ -31,7 +31,8 @@
 //                     product starts anew and joins O with the stage's V scale in
 //                     fp32, so scales of any ratio meet only in 32 bits.
 //     Positions outside the window and inside it go to separate partial states
-//     (m, l, o): a position is read once, local attention is the inside state, global
+//     (m, l, o; o as the mean of the values, so that no sum of states is larger than they
+//     are): a position is read once, local attention is the inside state, global
 //     attention both.  The warps of a CTA join their states in shared memory.
 //   decode8_combine_kernel  one CTA per query row, placed while the first kernel runs:
 //     joins the states of the CTAs that held a share of the row's stages, in the order of
@@ -285,12 +286,19 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 // Codes as fp16 pairs, exact.  e4m3: the code's value.  int8: (code + 128) 2^-24, a subnormal number whose bits are the code's with the sign bit turned; the
 // products' accumulators start at -128 2^-24 times the other operand's sum instead of zero.
 constexpr uint32_t kOnes = 0x3c003c00u;  // two fp16 ones
-// P's 2^16 and the codes' 2^-24 would take O out of range for values beyond 1e34: O is kept
-// without them, and the state's l is given the same factor when it is written.
+// O is held as kOScale times sum P v: with P's 2^14 the smallest values (scales of 2^-109) keep
+// their digits.  The V scale takes kVScale for it, int8's codes bring 2^-24 themselves.
 template <int TYPE>
 constexpr float kVScale = TYPE == kCacheE4M3 ? 1.f / 131072.f : 1.f;
 template <int TYPE>
-constexpr float kLScale = TYPE == kCacheE4M3 ? 1.f / 131072.f : 1.f / 16777216.f;
+constexpr float kOScale = TYPE == kCacheE4M3 ? 1.f / 131072.f : 1.f / 16777216.f;
+// A V scale up to kVsMax adds less than 2^96 to O with each position (P < 2^16, e4m3 codes < 2^9,
+// int8 codes up to 2^7), so that 2^30 positions stay below 2^126.  The first larger one of a run
+// takes a factor of kShrink off O and off every V scale from there on, which is enough for any
+// finite scale.
+template <int TYPE>
+constexpr float kVsMax = TYPE == kCacheE4M3 ? 0x1p88f : 0x1p97f;
+constexpr float kShrink = 0x1p-40f;
 constexpr float kInt8Unit = 16777216.f, kInt8Shift = -128.f / 16777216.f;
 
 template <int TYPE>
@@ -355,8 +363,10 @@ template <int D, int NT>
 struct State8 {
     float nr[NT][2], l[NT][2];
     float o[D / 16][NT][4];
+    float fx;  // 1, or kShrink
     __device__ __forceinline__ void init()
     {
+        fx = 1.f;
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt) nr[nt][0] = nr[nt][1] = kEmpty, l[nt][0] = l[nt][1] = 0.f;
         #pragma unroll
@@ -366,6 +376,15 @@ struct State8 {
     }
 };
 
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / x for a sum of weights x >= 0; 0 where there are none.
+__device__ __forceinline__ float share_of(float x) { return x == 0.f ? 0.f : fast_rcp(x); }
+
 __device__ __forceinline__ void store_if(bool yes, void* at, float a, float b)
 {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t@q st.v2.f32 [%1], {%2, %3};\n\t}" ::"r"((int)yes), "l"(at),
@@ -373,7 +392,8 @@ __device__ __forceinline__ void store_if(bool yes, void* at, float a, float b)
                  : "memory");
 }
 
-// The state's rows to (m, l) at ml[r] and o at o[r * D], in shared or global memory.  Predicated
+// The state's rows to (m, l) at ml[r] and o at o[r * D], in shared or global memory; o is written as
+// the mean sum P v / sum P, which is no larger than the values, however many they are.  Predicated
 // stores and no branches: this code runs once or twice in a launch, and every branch of it
 // would wait for its instructions.
 template <int TYPE, int D, int NT>
@@ -391,11 +411,12 @@ __device__ __forceinline__ void store_state8(State8<D, NT>& st, int R, float2* m
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int r = 8 * nt + 2 * t + c;
-            store_if(r < R && g == 0, ml + r, -st.nr[nt][c], st.l[nt][c] * kLScale<TYPE>);
+            const float f = share_of(st.l[nt][c] * (kOScale<TYPE> * st.fx));
+            store_if(r < R && g == 0, ml + r, -st.nr[nt][c], st.l[nt][c]);
             float* row = o + r * D + 2 * g;
             #pragma unroll
             for (int u = 0; u < D / 16; ++u)
-                store_if(r < R, row + 16 * u, st.o[u][nt][c], st.o[u][nt][2 + c]);
+                store_if(r < R, row + 16 * u, st.o[u][nt][c] * f, st.o[u][nt][2 + c] * f);
         }
 }
 
@@ -404,25 +425,27 @@ __device__ __forceinline__ void store_state8(State8<D, NT>& st, int R, float2* m
 template <int D, int NT>
 __device__ __forceinline__ void join_states(const Decode8Params& p, const uint8_t* at, int size, int rank, long long row)
 {
-    constexpr int C = D / 32;
+    constexpr int C = D / 32, kWarps = D8<D, NT>::kWarps;  // lanes 0 .. kWarps - 1 hold a warp's (m, l) each
     const int lane = threadIdx.x & 31;
     for (int r = rank; r < p.R; r += size) {
         auto ml = [&](int i) {
             return reinterpret_cast<const float2*>(at + (long long)i * D8<D, NT>::kWarpBytes + 8 * NT * D * 4)[r];
         };
-        const float mine = lane < size ? ml(lane).x : -INFINITY;
-        float m = mine;
+        const float2 mine = lane < size ? ml(lane) : make_float2(-INFINITY, 0.f);
+        float m = mine.x;
         #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float f_mine = mine == -INFINITY ? 0.f : exp2f(mine - m);
-        float l = 0.f, o[C];
+        for (int off = kWarps / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float w = mine.y * fast_exp2(mine.x - m);
+        float l = w, o[C];
+        #pragma unroll
+        for (int off = kWarps / 2; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        const float f_mine = w * share_of(l);
         #pragma unroll
         for (int c = 0; c < C; ++c) o[c] = 0.f;
         #pragma unroll 4
         for (int i = 0; i < size; ++i) {
             const float f = __shfl_sync(0xffffffffu, f_mine, i);
             const float* src = reinterpret_cast<const float*>(at + (long long)i * D8<D, NT>::kWarpBytes) + r * D + lane;
-            l = fmaf(f, ml(i).y, l);
             #pragma unroll
             for (int c = 0; c < C; ++c) o[c] = fmaf(f, src[32 * c], o[c]);
         }
@@ -593,7 +616,7 @@ __device__ __forceinline__ void place_nan(uint32_t tileV, int pos0, int lo0, int
 }
 
 // One stage: scores, softmax step, products.  `masked`: some column sees it in part, or the
-// V scale is not finite.
+// V scale is above kVsMax or not finite.
 template <int TYPE, int D, int NT>
 __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw, const uint2* qs, uint32_t tileK,
                                          float ks, float vs, bool masked, int pos0, int lo0, int hi0, int n)
@@ -606,7 +629,18 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
     if (masked) {
         if (mask_values<TYPE, D>(tileV, pos0, lo0, hi0, n) && TYPE == kCacheE4M3)
             place_nan<D, NT>(tileV, pos0, lo0, hi0, n, rw, st);
-        if (!finite(vs)) {
+        if (finite(vs)) {
+            if (fabsf(vs) > kVsMax<TYPE>) {
+                vs *= kShrink;
+                st.fx *= kShrink;
+                #pragma unroll
+                for (int u = 0; u < D / 16; ++u)
+                    #pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) st.o[u][nt][e] *= kShrink;
+            }
+        } else {
             // NaN for the columns that see the stage; the others' products are zero, which times
             // such a scale would be NaN too.
             #pragma unroll
@@ -896,13 +930,14 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
         }
         if (new_q) stage_q<TYPE, D, NT>(p, run >> 1, qs, rw);  // while the scales are on their way
         new_q = false;
-        const float ks = __shfl_sync(0xffffffffu, ks32, unit.y - first), vs = __shfl_sync(0xffffffffu, vs32, unit.y - first);
+        const float ks = __shfl_sync(0xffffffffu, ks32, unit.y - first);
+        const float vs = __shfl_sync(0xffffffffu, vs32, unit.y - first) * st.fx;
         const uint32_t parity = (ring.used / G::kStages) & 1;
         ok = mbar_try_wait(&ring.full[s], parity) || wait_long(&ring.full[s], parity, abort_flag, p.status, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int pos0 = unit.y * G::kStage;
-        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + G::kStage - 1 > hi0 || !finite(vs);
+        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + G::kStage - 1 > hi0 || !(fabsf(vs) <= kVsMax<TYPE>);
         do_stage<TYPE, D, NT>(st, rw, qs, ring.base + s * G::kStageBytes, ks, vs, masked, pos0, lo0, hi0, p.n);
         ++ring.used;
         __syncwarp();  // every lane is done with the stage
@@ -1013,7 +1048,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
     };
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // Each warp joins its states kJoin at a time, all of their loads in flight together; then
-    // warp 0 joins the warps'.
+    // warp 0 joins the warps'.  o is a mean of values throughout, l the sum of the weights.
     constexpr int kJoin = 8;
     float m[2], l[2], o[2][C];
     #pragma unroll
@@ -1060,19 +1095,24 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
         }
         #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const float f = weight(m[k], mx[k]);
+            const float was = weight(m[k], mx[k]) * l[k];
+            float w[kJoin];
             m[k] = mx[k];
-            l[k] *= f;
+            l[k] = was;
             #pragma unroll
-            for (int c = 0; c < C; ++c) o[k][c] *= f;
+            for (int j = 0; j < kJoin; ++j) {
+                w[j] = weight(s[j].x, mx[k]) * s[j].y;
+                l[k] = outside[j] == (k == 1) ? l[k] + w[j] : l[k];
+            }
+            const float f = share_of(l[k]);
+            #pragma unroll
+            for (int c = 0; c < C; ++c) o[k][c] *= was * f;
             #pragma unroll
             for (int j = 0; j < kJoin; ++j) {
                 // (a weight of zero does not hide a state that is NaN)
                 const bool here = outside[j] == (k == 1);
-                const float w = weight(s[j].x, mx[k]);
-                l[k] = here ? fmaf(w, s[j].y, l[k]) : l[k];
                 #pragma unroll
-                for (int c = 0; c < C; ++c) o[k][c] = here ? fmaf(w, v[j][c], o[k][c]) : o[k][c];
+                for (int c = 0; c < C; ++c) o[k][c] = here ? fmaf(w[j] * f, v[j][c], o[k][c]) : o[k][c];
             }
         }
     }
@@ -1087,32 +1127,39 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode8_combine_kernel(con
         if (warp > 0) return;
         #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float mx = m[k];
-            for (int w = 1; w < nw; ++w) mx = fmaxf(mx, red_m[k][w]);
-            const float f = weight(m[k], mx);
-            m[k] = mx;
-            l[k] *= f;
+            float x[kCombineWarps], w[kCombineWarps], mx = m[k];
             #pragma unroll
-            for (int c = 0; c < C; ++c) o[k][c] *= f;
-            for (int w = 1; w < nw; ++w) {
+            for (int i = 0; i < kCombineWarps; ++i) {
+                x[i] = i < nw ? red_m[k][i] : -INFINITY;
+                w[i] = i < nw ? red_l[k][i] : 0.f;
+                mx = fmaxf(mx, x[i]);
+            }
+            m[k] = mx;
+            l[k] = 0.f;
+            #pragma unroll
+            for (int i = 0; i < kCombineWarps; ++i) l[k] += w[i] *= weight(x[i], mx);
+            const float f = share_of(l[k]);
+            #pragma unroll
+            for (int c = 0; c < C; ++c) o[k][c] *= w[0] * f;
+            #pragma unroll
+            for (int i = 1; i < kCombineWarps; ++i) {
+                if (i >= nw) break;
                 float v[C];
-                load(&red_o[k][w][lane * C], v);
-                const float g = weight(red_m[k][w], mx);
-                l[k] = fmaf(g, red_l[k][w], l[k]);
+                load(&red_o[k][i][lane * C], v);
                 #pragma unroll
-                for (int c = 0; c < C; ++c) o[k][c] = fmaf(g, v[c], o[k][c]);
+                for (int c = 0; c < C; ++c) o[k][c] = fmaf(w[i] * f, v[c], o[k][c]);
             }
         }
     }
     float val[C];
     #pragma unroll
-    for (int c = 0; c < C; ++c) val[c] = l[0] == 0.f ? 0.f : o[0][c] / l[0];
+    for (int c = 0; c < C; ++c) val[c] = o[0][c];
     if (sel) {
         const float M = fmaxf(m[0], m[1]);
-        const float f0 = m[0] == -INFINITY ? 0.f : exp2f(m[0] - M), f1 = m[1] == -INFINITY ? 0.f : exp2f(m[1] - M);
-        const float lt = fmaf(f0, l[0], f1 * l[1]), share = 1.f / (1.f + expf(-gate));
+        const float w0 = weight(m[0], M) * l[0], w1 = weight(m[1], M) * l[1];
+        const float f = share_of(w0 + w1), share = 1.f / (1.f + expf(-gate));
         #pragma unroll
-        for (int c = 0; c < C; ++c) val[c] = fmaf(share, lt == 0.f ? 0.f : fmaf(f0, o[0][c], f1 * o[1][c]) / lt, val[c]);
+        for (int c = 0; c < C; ++c) val[c] = fmaf(share, fmaf(w0 * f, o[0][c], w1 * f * o[1][c]), val[c]);
     }
     uint32_t* dst = reinterpret_cast<uint32_t*>(out + lane * C);
     #pragma unroll
