@@ -1,0 +1,27 @@
+"""What the 8-bit cache's Python entry points refuse, on the host: each check comes before the library is called."""
+import pytest
+import torch
+
+import token_level_dynamic_seq_b200 as logo
+
+
+def step(n, gate, selected=None, B=2):
+    c = logo.cache8(B, 2, 200, 64, "cpu")
+    q = torch.zeros(B, 2, n, 64, dtype=torch.bfloat16)
+    return logo.decode8(q, c, torch.zeros(B, dtype=torch.int32), gate, torch.zeros(1), 16, selected=selected)
+
+
+@pytest.mark.parametrize("n,shape", [(1, (2, 4)), (1, (4,)), (1, (8,)), (1, (1, 2)), (3, (3, 2)), (3, (6,)), (3, (2, 4)),
+                                     (3, (2,)), (2, (2, 1)), (2, (2, 2, 1)), (1, ())])
+def test_gates_and_flags_of_another_shape(n, shape):
+    """A buffer of four gates a sequence with a step of one token, gates the other way round."""
+    with pytest.raises(ValueError, match="gate"):
+        step(n, torch.zeros(shape))
+    with pytest.raises(ValueError, match="selected"):
+        step(n, torch.zeros(2, n), torch.zeros(shape, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("n,shape", [(1, (2, 1)), (1, (2,)), (3, (2, 3))])
+def test_gates_of_the_right_shape_get_past(n, shape):
+    with pytest.raises(ValueError, match="CUDA"):     # the cache lies on the host
+        step(n, torch.zeros(shape), torch.zeros(shape, dtype=torch.int32))

@@ -185,11 +185,16 @@ def decode8_workspace(cache: Cache8, Hq: int, n: int = 1, stream=None) -> torch.
 def decode8(q, cache: Cache8, cache_len, gate, tau, window: int, ws=None, scale: float = 0.0, out=None, selected=None,
             stream=None):
     """Decode step over the cache: ``q`` bf16 [B, Hq, n, d] (or [B, Hq, d] for one token), ``cache_len`` int32 [B]
-    (the new tokens included), ``gate`` fp32 [B, n], ``tau`` fp32 [1].  Returns (out, like q; selected int32 [B, n])."""
+    (the new tokens included), ``gate`` fp32 [B, n], ``tau`` fp32 [1].  Returns (out, like q; selected int32 [B, n]).
+    A given ``selected`` has gate's shape; either may be [B] for one token."""
     B, Hq, *n, d = q.shape
     if len(n) > 1 or B != cache.B or d != cache.d:
         raise ValueError(f"q: expected [{cache.B}, Hq, n, {cache.d}], got {tuple(q.shape)}")
     n = n[0] if n else 1
+    # read by n from one sequence to the next: a longer buffer would give them each other's
+    for name, t in (("gate", gate), ("selected", selected)):
+        if t is not None and t.shape != (B, n) and not (n == 1 and t.shape == (B,)):
+            raise ValueError(f"{name}: expected [{B}, {n}], got {list(t.shape)}")
     lib = _lib_on(cache)
     if ws is None:
         ws = decode8_workspace(cache, Hq, n, stream)
