@@ -14,7 +14,8 @@ they were appended.  A serving loop is::
 As in the rest of the binding, only pointers are marshalled here; tensors have
 to lie on the current device.  Device-side errors go to the workspace's status
 word (:func:`check`): a call without ``ws`` makes one of its own, and its errors
-are not seen.
+are not seen.  A ``stream`` that is not the current one has to be ordered behind
+what made the inputs, and they have to be kept until it is done with them.
 """
 from __future__ import annotations
 
@@ -104,16 +105,20 @@ def _queue(cache: Cache8, stream):
     return torch._C._cuda_getCurrentRawStream(cache.index) if stream is None else stream.cuda_stream
 
 
-def _used_on(stream, *tensors):
-    """Tensors allocated here and used on `stream`: their memory is not given out again before it is done."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _new(stream, make):
+    """A tensor that a call on `stream` writes.  It is allocated there: memory that the current stream gave back may
+    still be in use by what is queued on it.  The caller goes on with the tensor on the current stream."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
 
 
 def _new_ws(cache: Cache8, size: int, stream):
-    ws = torch.empty(size, dtype=torch.uint8, device=cache.device)
-    _used_on(stream, ws)
+    ws = _new(stream, lambda: torch.empty(size, dtype=torch.uint8, device=cache.device))
     _logo._raise(_logo.load_library().logo_workspace_init(ws.data_ptr(), size, _logo._stream(stream)))
     return ws
 
@@ -160,8 +165,7 @@ def cache8_read(cache: Cache8, start, rows: int, ws=None, cu_seqlens=None, max_s
     rows = int(rows)
     want = (cache.B if cu_seqlens is None else 1, cache.Hkv, rows, cache.d)
     if out is None:
-        out = cache.k_tail.new_empty((2,) + want).unbind(0)
-        _used_on(stream, *out)
+        out = _new(stream, lambda: cache.k_tail.new_empty((2,) + want)).unbind(0)
     k, v = out
     if tuple(k.shape) != want or tuple(v.shape) != want:
         raise ValueError(f"out: expected {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
@@ -199,13 +203,11 @@ def decode8(q, cache: Cache8, cache_len, gate, tau, window: int, ws=None, scale:
     if ws is None:
         ws = decode8_workspace(cache, Hq, n, stream)
     if out is None:
-        out = torch.empty_like(q)
-        _used_on(stream, out)
+        out = _new(stream, lambda: torch.empty_like(q))
     elif out.shape != q.shape:
         raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
     if selected is None:
-        selected = cache_len.new_empty((B, n))
-        _used_on(stream, selected)
+        selected = _new(stream, lambda: cache_len.new_empty((B, n)))
     _logo._raise(lib.logo_decode8(
         _at(cache, q, torch.bfloat16, 0, "q"), cache._ref, _at(cache, cache_len, torch.int32, B, "cache_len"),
         _at(cache, gate, torch.float32, B * n, "gate"), _at(cache, tau, torch.float32, 1, "tau"), Hq, n, min(int(window), 0x7fffffff),
