@@ -66,7 +66,8 @@ typedef struct {
  *            start[b] may be the length so far, any multiple of `block` up to it,
  *            or, where the sequence's latest append went from s to e, a position
  *            from s to e whose block is one of the last two up to e.  Positions
- *            behind the new rows are given up.
+ *            behind the new rows are given up, also where n_b is 0 (every draft
+ *            rejected): the cache is then the one of the first start[b] tokens.
  *   new_len  int32 [B] (device) receiving start[b] + n_b, or NULL; apart from start.
  * k and v must be 32-byte aligned.  A sequence whose rows do not fit (start < 0
  * or start + n_b > Lmax), or whose packed offsets are out of order, beyond T or

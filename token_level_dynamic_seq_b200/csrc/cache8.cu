@@ -173,8 +173,9 @@ __global__ void __launch_bounds__(kA8ThreadsOf<D, BLOCK>, kA8Resident / kA8Threa
         if (!ok) atomicOr(p.status, kStatusBadArgument);
         if (p.new_len) p.new_len[b] = ok ? s + n : s;
     }
-    if (!ok || n == 0) return;
-    const int first = s / BLOCK, blk = first + j, end = s + n, last = (end - 1) / BLOCK;
+    if (!ok) return;
+    // (without new rows, what is left of the block is quantised without the rows taken back)
+    const int first = s / BLOCK, blk = first + j, end = s + n, last = (end + BLOCK - 1) / BLOCK - 1;
     if (blk > last) return;
     const int base = blk * BLOCK;
     const int kept = j == 0 ? s - base : 0;
