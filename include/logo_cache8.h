@@ -73,7 +73,8 @@ typedef struct {
  * or start + n_b > Lmax), or whose packed offsets are out of order, beyond T or
  * longer than max_seqlen, is left as it is (new_len = start) and reported:
  * logo_check gives LOGO_ERR_INVALID_ARG.  The workspace (256 bytes are enough)
- * carries the status word only.
+ * carries the status word only.  2 * B * Hkv times the blocks that the longest
+ * sequence can touch must stay below 2^31 (LOGO_ERR_UNSUPPORTED).
  */
 LOGO_API logo_status logo_cache8_append(const logo_cache8 *cache, const logo_bf16 *k, const logo_bf16 *v,
                                         const logo_shape *shape, const int32_t *start, int32_t *new_len, void *ws,

@@ -25,3 +25,17 @@ def test_gates_and_flags_of_another_shape(n, shape):
 def test_gates_of_the_right_shape_get_past(n, shape):
     with pytest.raises(ValueError, match="CUDA"):     # the cache lies on the host
         step(n, torch.zeros(shape), torch.zeros(shape, dtype=torch.int32))
+
+
+def test_more_blocks_than_a_grid_takes():
+    """2^20 pairs of a sequence and a head times 2^11 blocks and more: refused as unsupported, nothing is launched."""
+    import ctypes
+
+    lib = logo.load_library()
+    at = ctypes.c_void_p(1 << 20)
+    for block, longest in ((64, 1 << 16), (128, 1 << 17), (128, 1 << 20)):
+        c = logo.Cache8Desc(1 << 14, 1 << 6, 1 << 20, 64, block, 1, *[1 << 20] * 6)
+        rows = logo.Shape(1, 64, 64, 1 << 20, 64, 0x1000, 1 << 14, longest)
+        assert lib.logo_cache8_append(ctypes.byref(c), at, at, rows, at, None, at, 256, None) == 2
+        assert "blocks" in lib.logo_last_error().decode()
+        assert lib.logo_cache8_read(ctypes.byref(c), at, rows, at, at, at, 256, None) == 2

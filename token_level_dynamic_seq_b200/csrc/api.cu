@@ -413,6 +413,16 @@ logo_status check_rows_of(const logo_cache8* c, const logo_shape* sh, Geo& g)
     return LOGO_OK;
 }
 
+// Blocks of rows of all sequences, K and V, in one launch: as many as a grid takes.
+logo_status check_blocks(const logo_cache8* c, long long per_seq)
+{
+    const long long pairs = 2LL * c->B * c->Hkv;
+    if (per_seq > 0x7fffffffLL / pairs)
+        return fail(LOGO_ERR_UNSUPPORTED, "2 * B * Hkv = %lld times %lld blocks of the longest sequence exceeds 2^31 - 1",
+                    pairs, per_seq);
+    return LOGO_OK;
+}
+
 logo_status check_rows8(const logo_cache8* c, int Hq, int n)
 {
     if (Hq < 1 || n < 1) return fail(LOGO_ERR_INVALID_ARG, "Hq=%d n=%d out of range", Hq, n);
@@ -862,6 +872,8 @@ logo_status logo_cache8_append(const logo_cache8* cache, const logo_bf16* k, con
     // Every CTA reads start while one writes new_len.
     if (new_len && new_len < start + cache->B && start < new_len + cache->B)
         return fail(LOGO_ERR_INVALID_ARG, "new_len overlaps start");
+    const long long nb = ((long long)g.max_len + 2 * cache->block - 2) / cache->block;  // a block's last row first
+    if ((st = check_blocks(cache, nb)) != LOGO_OK) return st;
     logo::Append8Params p;
     memset(&p, 0, sizeof p);
     p.c = view_of(cache);
@@ -873,7 +885,7 @@ logo_status logo_cache8_append(const logo_cache8* cache, const logo_bf16* k, con
     p.status = static_cast<uint32_t*>(ws);
     p.n = g.L;
     p.max_n = g.max_len;
-    p.nb = (int)(((long long)g.max_len + 2 * cache->block - 2) / cache->block);  // a block's last row first
+    p.nb = (int)nb;
     NvtxRange range("logo cache append");
     cudaError_t e = logo::launch_append8(p, cache->type, cache->d, cache->block, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LOGO_OK : cuda_fail(e, "cache append launch");
@@ -889,6 +901,8 @@ logo_status logo_cache8_read(const logo_cache8* cache, const int32_t* start, con
     if ((st = check_ptr(start, "start", 4)) != LOGO_OK) return st;
     if (g.L > 0 && ((st = check_ptr(k_out, "k_out", 32)) != LOGO_OK || (st = check_ptr(v_out, "v_out", 32)) != LOGO_OK))
         return st;
+    const long long nb = g.max_len > 0 ? ((long long)g.max_len + logo::kRead8Rows - 1) / logo::kRead8Rows : 1;
+    if ((st = check_blocks(cache, nb)) != LOGO_OK) return st;
     logo::Read8Params p;
     memset(&p, 0, sizeof p);
     p.c = view_of(cache);
@@ -899,6 +913,7 @@ logo_status logo_cache8_read(const logo_cache8* cache, const int32_t* start, con
     p.status = static_cast<uint32_t*>(ws);
     p.n = g.L;
     p.max_n = g.max_len;
+    p.nb = (int)nb;
     NvtxRange range("logo cache read");
     cudaError_t e = logo::launch_read8(p, cache->type, cache->d, cache->block, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LOGO_OK : cuda_fail(e, "cache read launch");

@@ -46,7 +46,6 @@ template <int D, int BLOCK>
 constexpr int kA8ThreadsOf = D * BLOCK > 8192 ? 256 : 128;
 constexpr int kA8Resident = 1024;  // threads per SM, by the registers of a thread (64)
 constexpr int kR8Threads = 128;
-constexpr int kR8Rows = 64;  // rows per CTA of the read
 
 template <int TYPE>
 struct Q8;
@@ -305,17 +304,17 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return r;
 }
 
-// One CTA per (sequence, key/value head, K or V, kR8Rows rows); every load of a
+// One CTA per (sequence, key/value head, K or V, kRead8Rows rows); every load of a
 // thread is issued before its first use.
 template <int TYPE, int D, int BLOCK>
-__global__ void __launch_bounds__(kR8Threads) read8_kernel(const __grid_constant__ Read8Params p, int nb)
+__global__ void __launch_bounds__(kR8Threads) read8_kernel(const __grid_constant__ Read8Params p)
 {
     constexpr int kVecRow = D / 16;
-    constexpr int kVec = kR8Rows * kVecRow / kR8Threads;
+    constexpr int kVec = kRead8Rows * kVecRow / kR8Threads;
     const int Hkv = p.c.Hkv;
     long long it = blockIdx.x;
-    const int j = (int)(it % nb);
-    it /= nb;
+    const int j = (int)(it % p.nb);
+    it /= p.nb;
     const int kv = (int)(it & 1);
     it >>= 1;
     const int hk = (int)(it % Hkv), b = (int)(it / Hkv);
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(kR8Threads) read8_kernel(const __grid_constant
         if (j == 0 && kv == 0 && hk == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusBadArgument);
         return;
     }
-    const int r0 = j * kR8Rows, rows = n - r0 < kR8Rows ? n - r0 : kR8Rows;
+    const int r0 = j * kRead8Rows, rows = n - r0 < kRead8Rows ? n - r0 : kRead8Rows;
     if (rows <= 0) return;
     const long long slab = (long long)b * Hkv + hk;
     const uint8_t* code = p.c.code[kv] + (slab * p.c.Lmax + s + r0) * D;
@@ -367,22 +366,21 @@ cudaError_t append_td(const Append8Params& p, int block, unsigned grid, cudaStre
 }
 
 template <int TYPE, int D>
-cudaError_t read_td(const Read8Params& p, int block, unsigned grid, int nb, cudaStream_t stream)
+cudaError_t read_td(const Read8Params& p, int block, unsigned grid, cudaStream_t stream)
 {
     if (block == 64)
-        read8_kernel<TYPE, D, 64><<<grid, kR8Threads, 0, stream>>>(p, nb);
+        read8_kernel<TYPE, D, 64><<<grid, kR8Threads, 0, stream>>>(p);
     else
-        read8_kernel<TYPE, D, 128><<<grid, kR8Threads, 0, stream>>>(p, nb);
+        read8_kernel<TYPE, D, 128><<<grid, kR8Threads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+// (the grids fit 31 bits: checked by the callers)
 cudaError_t launch_append8(const Append8Params& p, int type, int d, int block, cudaStream_t stream)
 {
-    const long long items = (long long)p.c.B * p.c.Hkv * 2 * p.nb;
-    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)items;
+    const unsigned grid = (unsigned)((long long)p.c.B * p.c.Hkv * 2 * p.nb);
     if (type == kCacheE4M3)
         return d == 64 ? append_td<kCacheE4M3, 64>(p, block, grid, stream)
                        : append_td<kCacheE4M3, 128>(p, block, grid, stream);
@@ -392,15 +390,12 @@ cudaError_t launch_append8(const Append8Params& p, int type, int d, int block, c
 
 cudaError_t launch_read8(const Read8Params& p, int type, int d, int block, cudaStream_t stream)
 {
-    const int nb = (p.max_n + kR8Rows - 1) / kR8Rows;
-    const long long items = (long long)p.c.B * p.c.Hkv * 2 * (nb > 0 ? nb : 1);
-    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)items;
+    const unsigned grid = (unsigned)((long long)p.c.B * p.c.Hkv * 2 * p.nb);
     if (type == kCacheE4M3)
-        return d == 64 ? read_td<kCacheE4M3, 64>(p, block, grid, nb > 0 ? nb : 1, stream)
-                       : read_td<kCacheE4M3, 128>(p, block, grid, nb > 0 ? nb : 1, stream);
-    return d == 64 ? read_td<kCacheInt8, 64>(p, block, grid, nb > 0 ? nb : 1, stream)
-                   : read_td<kCacheInt8, 128>(p, block, grid, nb > 0 ? nb : 1, stream);
+        return d == 64 ? read_td<kCacheE4M3, 64>(p, block, grid, stream)
+                       : read_td<kCacheE4M3, 128>(p, block, grid, stream);
+    return d == 64 ? read_td<kCacheInt8, 64>(p, block, grid, stream)
+                   : read_td<kCacheInt8, 128>(p, block, grid, stream);
 }
 
 }  // namespace logo

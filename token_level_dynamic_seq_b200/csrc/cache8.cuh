@@ -40,7 +40,9 @@ struct Read8Params {
     const int32_t* cu_seqlens;  // nullptr: fixed length
     uint32_t* status;
     int n, max_n;
+    int nb;  // blocks of kRead8Rows rows of the longest sequence
 };
+constexpr int kRead8Rows = 64;  // rows per CTA of the read
 
 cudaError_t launch_append8(const Append8Params& p, int type, int d, int block, cudaStream_t stream);
 cudaError_t launch_read8(const Read8Params& p, int type, int d, int block, cudaStream_t stream);
