@@ -39,3 +39,15 @@ def test_more_blocks_than_a_grid_takes():
         assert lib.logo_cache8_append(ctypes.byref(c), at, at, rows, at, None, at, 256, None) == 2
         assert "blocks" in lib.logo_last_error().decode()
         assert lib.logo_cache8_read(ctypes.byref(c), at, rows, at, at, at, 256, None) == 2
+
+
+def test_workspace_of_a_cache_that_is_not_on_the_current_device(monkeypatch):
+    """The workspace is cleared on the current device's stream: for a cache elsewhere that would be in no order with the
+    calls that use it."""
+    with pytest.raises(ValueError, match="CUDA"):
+        logo.decode8_workspace(logo.cache8(2, 2, 200, 64, "cpu"), 2)
+    other = logo.cache8(2, 2, 200, 64, "cpu")
+    other.index = 7                                    # as a cache on another device says
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device"):
+        logo.decode8_workspace(other, 2)

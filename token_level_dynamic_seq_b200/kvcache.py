@@ -183,6 +183,7 @@ def decode8_workspace(cache: Cache8, Hq: int, n: int = 1, stream=None) -> torch.
     size = _logo.load_library().logo_decode8_workspace_size(cache._ref, int(Hq), int(n))
     if size == 0:
         raise _logo.LogoError(2, _logo.load_library().logo_last_error().decode())
+    _lib_on(cache)
     return _new_ws(cache, size, stream)
 
 
