@@ -34,9 +34,10 @@
 //     (m, l, o; o as the mean of the values, so that no sum of states is larger than they
 //     are): a position is read once, local attention is the inside state, global
 //     attention both.  The warps of a CTA join their states in shared memory.
-//   decode8_combine_kernel  one CTA per query row, placed while the first kernel runs:
-//     joins the states of the CTAs that held a share of the row's stages, in the order of
-//     the list; o = local + sigmoid(g) * global, one rounding.
+//   decode8_combine_kernel  one CTA per query row, placed while the first kernel runs where
+//     that leaves registers (up to 8 rows; up to 16 at d = 64): joins the states of the CTAs
+//     that held a share of the row's stages, in the order of the list;
+//     o = local + sigmoid(g) * global, one rounding.
 //
 // mma.sync and not tcgen05: a stage of 8 KB takes an SM about 350 cycles to fetch and its
 // 32 products a fraction of that, and codes need a conversion in registers, which an
@@ -45,17 +46,23 @@
 // Roundings: q is scaled by a power of two per row, so that its largest element lies
 // in [2^14, 2^15), and rounded to fp16 (exact for elements down to 2^-28 of the
 // largest).  P is held near 2^14 times itself in fp16: 11 bits, 3 more than bf16, with
-// values down to 2^-38 of the largest kept.  The sum l uses the unrounded P.
+// values down to 2^-38 of the largest kept.  The sum l uses the unrounded P.  int8 codes enter
+// the products as code + 128, less 128 times the other operand's sum: the fp32 roundings of a
+// product go with up to 383 code steps where the codes may be zero (a score is off by
+// (d / 16 + 3) 2^-22 * 383 scale sum |q| code steps at most, where the codes' own half steps may
+// make 256 times that).
 //
 // Measured (d = 128, 32 query heads on 8, e4m3, window 4096; bytes that have to be read
-// over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 219 us
-// (0.91; 195 to 215 where a call finds what the one before left in L2);
-// one global sequence of 128K beside a local one 50.5 us (0.84); one of 32K 19.3 us (0.53);
-// 16 of 8K to 32K with four drafted tokens each 58.8 us (0.68); two of 4K 9.2 us.  Once its
-// first bytes are there (5 us: launch, lengths, the first 19 MB of all SMs' rings), a warp
-// takes 2,650 to 3,000 cycles a stage, of which HBM alone asks 2,850; the kernel's end and
-// the combine take 4 us.  With 16 rows and more the issue of a stage's instructions is as
-// long as its fetch (370 MB for 4, 16, 24 and 32 rows a key/value head: 62, 74, 100, 122 us).
+// over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 220 us
+// (0.90; 195 where a call finds what the one before left in L2); one global sequence of 128K
+// beside a local one 50.0 us (0.84); one of 32K 19.2 us (0.53); 16 of 8K to 32K with four
+// drafted tokens each 58.5 us (0.69); two of 4K 9.0 us.  Once its first bytes are there (5 us:
+// launch, lengths, the first 19 MB of all SMs' rings), a warp takes 2,650 to 3,000 cycles a
+// stage, of which HBM alone asks 2,850; the kernel's end and the combine take 4 us.  From 9 rows
+// on a warp's way through a stage (ldmatrix, conversion, products, softmax, movmatrix, products)
+// is longer than its fetch, and with two warps a scheduler much of its latency shows: issue slots
+// 39 to 44 % busy, tensor pipe 31 to 39 %, the largest stalls fixed latencies and the tensor pipe
+// (370 MB for 4, 16, 24 and 32 rows a key/value head: 63, 74, 97, 118 us; int8 63, 77, 104, 129).
 // A maximum for every stage in place of kPMargin: four drafts 64.6 us, 32 rows 185 us (with
 // the six warps that its registers allowed), one token the same.
 // Tried and left out: 64-position stages at d = 128 (four drafts 70 us), paired fp32
@@ -101,9 +108,9 @@ struct D8 {
     static constexpr int kStateBytes = 8 * NT * (D + 2) * 4;      // partial state, written over the ring at the end
     static constexpr int kUsedBytes = kRingBytes + kQBytes > kStateBytes ? kRingBytes + kQBytes : kStateBytes;
     static constexpr int kWarpBytes = (kUsedBytes + 1023) / 1024 * 1024;
-    // Two warps on every scheduler, and (up to 16 rows) registers and shared memory left for
-    // the combine kernel's CTAs (12 warps: they wait for the others to end, 10.4 -> 13.9 us for
-    // short contexts, 21.0 -> 25.0 us for one of 32K).
+    // Two warps on every scheduler, and (up to 8 rows; 16 at d = 64) registers and shared memory
+    // left for the combine kernel's CTAs (12 warps: they wait for the others to end, 10.4 -> 13.9
+    // us for short contexts, 21.0 -> 25.0 us for one of 32K).
     static constexpr int kWarps = 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSmem = kWarps * kWarpBytes + 1024;      // + alignment slack
@@ -212,8 +219,10 @@ __device__ __forceinline__ int* prefix_of(const Decode8Params& p)
     return reinterpret_cast<int*>(p.part) - prefix8(p.B);
 }
 // Sequences up to which a CTA of the combine kernel adds up the lengths itself, while the
-// partial kernel runs (10.0 us for short contexts, else 10.6); above that the sums of all its
-// CTAs took as long as the attention (512 short sequences: combine 57 us).
+// partial kernel runs, and above which it reads the sums that CTA 0 of that wrote.  Either way
+// for 512 positions of 2 heads, 4 rows (us): 2 sequences 7.4 and 7.8, 32 8.8 and 9.3, 64 11.5 and
+// 11.7, 96 13.5 and 13.6, 128 15.4 and 15.3, 256 24.5 and 21.5, 1,024 97 and 68; with 24 rows
+// at d = 64: 64 17.9 and 17.8, 128 27.1 and 24.9.
 constexpr int kScanMax = 64;
 
 // Partial states lie in slots of R rows and two kinds, (m, l) and o apart.  Slot (warp of
