@@ -51,3 +51,12 @@ def test_workspace_of_a_cache_that_is_not_on_the_current_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
         logo.decode8_workspace(other, 2)
+
+
+@pytest.mark.parametrize("shape", [(2,), (0,), (2, 1)])
+def test_more_than_one_threshold(shape):
+    """One threshold serves the batch: of several the first would be taken for all."""
+    c = logo.cache8(2, 2, 200, 64, "cpu")
+    with pytest.raises(ValueError, match="tau"):
+        logo.decode8(torch.zeros(2, 2, 1, 64, dtype=torch.bfloat16), c, torch.zeros(2, dtype=torch.int32), torch.zeros(2, 1),
+                     torch.zeros(shape), 16)

@@ -200,6 +200,8 @@ def decode8(q, cache: Cache8, cache_len, gate, tau, window: int, ws=None, scale:
     for name, t in (("gate", gate), ("selected", selected)):
         if t is not None and t.shape != (B, n) and not (n == 1 and t.shape == (B,)):
             raise ValueError(f"{name}: expected [{B}, {n}], got {list(t.shape)}")
+    if tau.numel() != 1:
+        raise ValueError(f"tau: expected one element, got {tau.numel()}")
     lib = _lib_on(cache)
     if ws is None:
         ws = decode8_workspace(cache, Hq, n, stream)
