@@ -112,8 +112,6 @@ LOGO_API logo_status logo_cache8_read(const logo_cache8 *cache, const int32_t *s
  * logo_decode8_workspace_size(cache, Hq, n) bytes (0 if they are not supported),
  * be set up once with logo_workspace_init, and be used by one stream (or one
  * captured graph) at a time.
- * Scores are held in fp32; with int8 the largest |q| times the largest |k| times
- * the scale must stay below 2^124.
  * A key, value or scale that is not finite reaches the tokens that attend to its
  * position (a scale's: its block) and no others; a value's scale that is not
  * finite makes their outputs NaN.

@@ -46,11 +46,11 @@
 // Roundings: q is scaled by a power of two per row, so that its largest element lies
 // in [2^14, 2^15), and rounded to fp16 (exact for elements down to 2^-28 of the
 // largest).  P is held near 2^14 times itself in fp16: 11 bits, 3 more than bf16, with
-// values down to 2^-38 of the largest kept.  The sum l uses the unrounded P.  int8 codes enter
-// the products as code + 128, less 128 times the other operand's sum: the fp32 roundings of a
-// product go with up to 383 code steps where the codes may be zero (a score is off by
-// (d / 16 + 3) 2^-22 * 383 scale sum |q| code steps at most, where the codes' own half steps may
-// make 256 times that).
+// values down to 2^-38 of the largest kept.  The sum l uses the unrounded P.  The codes are
+// exact: int8 codes as code + 128 in the products, less 128 times the other operand's sum, save
+// two instructions of five for every four codes, but the roundings of sums that large stay
+// where the codes are zero (16 rows: 77.4 against 80.5 us, four 61.1 against 61.9; d = 64, 32
+// rows 78.2 against 74.7, where the correction costs more than it saves).
 //
 // Measured (d = 128, 32 query heads on 8, e4m3, window 4096; bytes that have to be read
 // over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 220 us
@@ -62,7 +62,7 @@
 // on a warp's way through a stage (ldmatrix, conversion, products, softmax, movmatrix, products)
 // is longer than its fetch, and with two warps a scheduler much of its latency shows: issue slots
 // 39 to 44 % busy, tensor pipe 31 to 39 %, the largest stalls fixed latencies and the tensor pipe
-// (370 MB for 4, 16, 24 and 32 rows a key/value head: 63, 74, 97, 118 us; int8 63, 77, 104, 129).
+// (370 MB for 4, 16, 24 and 32 rows a key/value head: 63, 74, 97, 118 us; int8 64, 80, 103, 131).
 // A maximum for every stage in place of kPMargin: four drafts 64.6 us, 32 rows 185 us (with
 // the six warps that its registers allowed), one token the same.
 // Tried and left out: 64-position stages at d = 128 (four drafts 70 us), paired fp32
@@ -274,15 +274,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The same from C = (c0, c1, c2, c3) (a zero costs no register).
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                             uint32_t b1, float c0, float c1, float c2, float c3)
+// The same from zero (which costs no register).
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1)
 {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %11, %12, %13};"
+        "{%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
@@ -292,23 +292,21 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-// Codes as fp16 pairs, exact.  e4m3: the code's value.  int8: (code + 128) 2^-24, a subnormal number whose bits are the code's with the sign bit turned; the
-// products' accumulators start at -128 2^-24 times the other operand's sum instead of zero.
-constexpr uint32_t kOnes = 0x3c003c00u;  // two fp16 ones
-// O is held as kOScale times sum P v: with P's 2^14 the smallest values (scales of 2^-109) keep
-// their digits.  The V scale takes kVScale for it, int8's codes bring 2^-24 themselves.
-template <int TYPE>
-constexpr float kVScale = TYPE == kCacheE4M3 ? 1.f / 131072.f : 1.f;
-template <int TYPE>
-constexpr float kOScale = TYPE == kCacheE4M3 ? 1.f / 131072.f : 1.f / 16777216.f;
-// A V scale up to kVsMax adds less than 2^96 to O with each position (P < 2^16, e4m3 codes < 2^9,
-// int8 codes up to 2^7), so that 2^30 positions stay below 2^126.  The first larger one of a run
-// takes a factor of kShrink off O and off every V scale from there on, which is enough for any
-// finite scale.
-template <int TYPE>
-constexpr float kVsMax = TYPE == kCacheE4M3 ? 0x1p88f : 0x1p97f;
-constexpr float kShrink = 0x1p-40f;
-constexpr float kInt8Unit = 16777216.f, kInt8Shift = -128.f / 16777216.f;
+// O is held as kOScale times sum P v (the V scale takes it along): with P's 2^14 the smallest
+// values (scales of 2^-109) keep their digits.
+constexpr float kOScale = 0x1p-17f;
+// A V scale up to kVsMax adds less than 2^96 to O with each position (P < 2^16, codes < 2^9), so
+// that 2^30 positions stay below 2^126.  The first larger one of a run takes a factor of kShrink
+// off O and off every V scale from there on, which is enough for any finite scale.
+constexpr float kVsMax = 0x1p88f, kShrink = 0x1p-40f;
+
+// Codes as fp16 pairs, exact.  int8: a code + 128 as the low byte of fp16's 1024 is 1152 + code.
+__device__ __forceinline__ uint32_t less_1152(uint32_t x)
+{
+    uint32_t y;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x64806480u));
+    return y;
+}
 
 template <int TYPE>
 __device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)  // bytes 0, 1 and 2, 3
@@ -322,8 +320,8 @@ __device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)  
             : "r"(w));
     } else {
         const uint32_t u = w ^ 0x80808080u;
-        lo = __byte_perm(u, 0u, 0x4140);
-        hi = __byte_perm(u, 0u, 0x4342);
+        lo = less_1152(__byte_perm(u, 0x64646464u, 0x4140));
+        hi = less_1152(__byte_perm(u, 0x64646464u, 0x4342));
     }
 }
 
@@ -337,8 +335,8 @@ __device__ __forceinline__ void to_f16_pairs(uint32_t w, uint32_t& even, uint32_
         to_f16<TYPE>(__byte_perm(w, 0u, 0x3120), even, odd);
     } else {
         const uint32_t u = w ^ 0x80808080u;
-        even = __byte_perm(u, 0u, 0x4240);
-        odd = __byte_perm(u, 0u, 0x4341);
+        even = less_1152(__byte_perm(u, 0x64646464u, 0x4240));
+        odd = less_1152(__byte_perm(u, 0x64646464u, 0x4341));
     }
 }
 
@@ -420,7 +418,7 @@ __device__ __forceinline__ void store_state8(State8<D, NT>& st, int R, float2* m
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int r = 8 * nt + 2 * t + c;
-            const float f = share_of(st.l[nt][c] * (kOScale<TYPE> * st.fx));
+            const float f = share_of(st.l[nt][c] * (kOScale * st.fx));
             store_if(r < R && g == 0, ml + r, -st.nr[nt][c], st.l[nt][c]);
             float* row = o + r * D + 2 * g;
             #pragma unroll
@@ -508,9 +506,7 @@ __device__ __forceinline__ void issue_unit(const Decode8Params& p, Ring8& ring, 
 // Per-lane constants of the (sequence, key/value head) at hand.
 template <int NT>
 struct Rows8 {
-    float qf[NT][2];  // scale * log2(e) / (the power of two in the row's fp16 q); int8's 2^24 apart: together
-                      // they pass 2^127 for q from 1e36 on, where the key's scale brings them back
-    float s0[NT][2];  // what the scores' accumulators start at (int8)
+    float qf[NT][2];  // scale * log2(e) / (the power of two in the row's fp16 q)
     int tok[NT][2];   // the column's token
 };
 
@@ -539,28 +535,17 @@ __device__ __forceinline__ void stage_q(const Decode8Params& p, long long pair, 
         int ex = 141 - (int)(big >> 7);  // largest element into [2^14, 2^15)
         ex = ex > 126 ? 126 : ex;
         const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-        float sum = 0.f;  // of the row's fp16 values
         #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             uint2 f;
             f.x = pack_f16x2(__uint_as_float(w[kk].x << 16) * up, __uint_as_float(w[kk].x & 0xffff0000u) * up);
             f.y = pack_f16x2(__uint_as_float(w[kk].y << 16) * up, __uint_as_float(w[kk].y & 0xffff0000u) * up);
             qs[(kk * NT + nt) * 32 + lane] = f;
-            if (TYPE == kCacheInt8) {
-                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&f.x));
-                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&f.y));
-                sum += (a.x + a.y) + (b.x + b.y);
-            }
-        }
-        if (TYPE == kCacheInt8) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         }
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int e2 = __shfl_sync(0xffffffffu, ex, 4 * (2 * t + c));
             rw.qf[nt][c] = p.scale_log2 * __uint_as_float((uint32_t)(127 - e2) << 23);
-            rw.s0[nt][c] = TYPE == kCacheInt8 ? kInt8Shift * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + c)) : 0.f;
         }
     }
     __syncwarp();
@@ -639,7 +624,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
         if (mask_values<TYPE, D>(tileV, pos0, lo0, hi0, n) && TYPE == kCacheE4M3)
             place_nan<D, NT>(tileV, pos0, lo0, hi0, n, rw, st);
         if (finite(vs)) {
-            if (fabsf(vs) > kVsMax<TYPE>) {
+            if (fabsf(vs) > kVsMax) {
                 vs *= kShrink;
                 st.fx *= kShrink;
                 #pragma unroll
@@ -689,8 +674,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if (kk == 0)
-                    mma_f16_from(sc[mt][nt], x[mt][0], x[mt][1], y[mt][0], y[mt][1], b0[nt].x, b0[nt].y, rw.s0[nt][0],
-                                 rw.s0[nt][1], rw.s0[nt][0], rw.s0[nt][1]);
+                    mma_f16_zero(sc[mt][nt], x[mt][0], x[mt][1], y[mt][0], y[mt][1], b0[nt].x, b0[nt].y);
                 else
                     mma_f16(sc[mt][nt], x[mt][0], x[mt][1], y[mt][0], y[mt][1], b0[nt].x, b0[nt].y);
             }
@@ -709,7 +693,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
     for (int nt = 0; nt < NT; ++nt)
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const float f = ks * rw.qf[nt][c] * (TYPE == kCacheInt8 ? kInt8Unit : 1.f);
+            const float f = ks * rw.qf[nt][c];
             #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
                 #pragma unroll
@@ -763,20 +747,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
                 pb[mt][nt][h] = movm(pack_f16x2(x[0], x[1]));
             }
     // O^T += (V^T P^T) vs
-    float o0[NT][2];  // what the products start at: zero, or (int8) -128 2^-24 sum P
-    #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        o0[nt][0] = o0[nt][1] = 0.f;
-        if (TYPE == kCacheInt8) {
-            float ones[4];
-            mma_f16_from(ones, kOnes, kOnes, kOnes, kOnes, pb[0][nt][0], pb[0][nt][1], 0.f, 0.f, 0.f, 0.f);
-            #pragma unroll
-            for (int mt = 1; mt < MT; ++mt) mma_f16(ones, kOnes, kOnes, kOnes, kOnes, pb[mt][nt][0], pb[mt][nt][1]);
-            o0[nt][0] = ones[0] * kInt8Shift;
-            o0[nt][1] = ones[1] * kInt8Shift;
-        }
-    }
-    vs *= kVScale<TYPE>;
+    vs *= kOScale;
     const uint32_t vat = swz<D>(tileV, lane, 0);
     #pragma unroll
     for (int u = 0; u < D / 16; ++u) {
@@ -794,8 +765,7 @@ __device__ __forceinline__ void do_stage(State8<D, NT>& st, const Rows8<NT>& rw,
         float acc[NT][4];
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            mma_f16_from(acc[nt], ev[0][0], od[0][0], ev[0][1], od[0][1], pb[0][nt][0], pb[0][nt][1], o0[nt][0], o0[nt][1],
-                         o0[nt][0], o0[nt][1]);
+            mma_f16_zero(acc[nt], ev[0][0], od[0][0], ev[0][1], od[0][1], pb[0][nt][0], pb[0][nt][1]);
         #pragma unroll
         for (int mt = 1; mt < MT; ++mt)
             #pragma unroll
@@ -946,7 +916,7 @@ __global__ void __launch_bounds__(D8<D, NT>::kThreads, 1) decode8_partial_kernel
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int pos0 = unit.y * G::kStage;
-        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + G::kStage - 1 > hi0 || !(fabsf(vs) <= kVsMax<TYPE>);
+        const bool masked = pos0 < lo0 + p.n - 1 || pos0 + G::kStage - 1 > hi0 || !(fabsf(vs) <= kVsMax);
         do_stage<TYPE, D, NT>(st, rw, qs, ring.base + s * G::kStageBytes, ks, vs, masked, pos0, lo0, hi0, p.n);
         ++ring.used;
         __syncwarp();  // every lane is done with the stage
