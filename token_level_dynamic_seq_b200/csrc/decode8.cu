@@ -54,15 +54,15 @@
 //
 // Measured (d = 128, 32 query heads on 8, e4m3, window 4096; bytes that have to be read
 // over the time, of the measured 6568 GB/s): 64 sequences of 32K, 13 global, 220 us
-// (0.90; 195 where a call finds what the one before left in L2); one global sequence of 128K
-// beside a local one 50.0 us (0.84); one of 32K 19.2 us (0.53); 16 of 8K to 32K with four
-// drafted tokens each 58.5 us (0.69); two of 4K 9.0 us.  Once its first bytes are there (5 us:
+// (0.90; 195 to 216 where a call finds what the one before left in L2); one global sequence of 128K
+// beside a local one 50.1 us (0.84); one of 32K 19.0 us (0.54); 16 of 8K to 32K with four
+// drafted tokens each 58.4 us (0.69); two of 4K 8.9 us.  Once its first bytes are there (5 us:
 // launch, lengths, the first 19 MB of all SMs' rings), a warp takes 2,650 to 3,000 cycles a
 // stage, of which HBM alone asks 2,850; the kernel's end and the combine take 4 us.  From 9 rows
 // on a warp's way through a stage (ldmatrix, conversion, products, softmax, movmatrix, products)
 // is longer than its fetch, and with two warps a scheduler much of its latency shows: issue slots
-// 39 to 44 % busy, tensor pipe 31 to 39 %, the largest stalls fixed latencies and the tensor pipe
-// (370 MB for 4, 16, 24 and 32 rows a key/value head: 63, 74, 97, 118 us; int8 64, 80, 103, 131).
+// 38 to 46 % busy, tensor pipe 26 to 39 %, the largest stalls fixed latencies and the tensor pipe
+// (370 MB for 4, 16, 24 and 32 rows a key/value head: 63, 74, 97, 118 us; int8 63, 80, 103, 131).
 // A maximum for every stage in place of kPMargin: four drafts 64.6 us, 32 rows 185 us (with
 // the six warps that its registers allowed), one token the same.
 // Tried and left out: 64-position stages at d = 128 (four drafts 70 us), paired fp32
